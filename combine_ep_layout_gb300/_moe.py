@@ -1,0 +1,255 @@
+"""ctypes binding of the decode-side MoE operators (include/ep_gb300_moe.h): the
+router and its gradient, products with 4-bit weights, and a whole MoE layer for
+a few tokens.  Argument checks and marshalling only, as in _native.
+"""
+import ctypes
+
+import torch
+
+from ._native import (EP_BF16, EP_EINVAL, EP_FP32, EpError, _check, _ptr, _require, _stream_ptr,
+                      load_library)
+
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+EP_INT4X2 = 4
+EP_ACT_SILU, EP_ACT_GELU_TANH = 0, 1
+EP_FEW_TOKENS = 64
+
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+_WEIGHTS = {"bf16": EP_BF16, "int4": EP_INT4X2, "int4x2": EP_INT4X2}
+_ACTS = {"silu": EP_ACT_SILU, "gelu_tanh": EP_ACT_GELU_TANH}
+_FLOATS = {torch.bfloat16: EP_BF16, torch.float32: EP_FP32}
+
+
+class ep_route_cfg_t(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class ep_moe_cfg_t(ctypes.Structure):
+    _fields_ = [("hidden_dim", ctypes.c_int32), ("intermediate_dim", ctypes.c_int32),
+                ("num_experts", ctypes.c_int32), ("num_expert_per_token", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("group_size", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class ep_moe_weights_t(ctypes.Structure):
+    _fields_ = [("w13", ctypes.c_void_p), ("w13_scales", ctypes.c_void_p),
+                ("w2", ctypes.c_void_p), ("w2_scales", ctypes.c_void_p)]
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = load_library()
+    c = ctypes
+    vp, i32, i64 = c.c_void_p, c.c_int32, c.c_int64
+    rc, mw = c.POINTER(ep_route_cfg_t), c.POINTER(ep_moe_weights_t)
+    L.ep_route.argtypes = [rc, vp, i32, i64, vp, i32, vp, vp, vp]
+    L.ep_route_backward.argtypes = [rc, vp, i32, i64, vp, vp, i32, vp, i64, vp]
+    L.ep_w4_linear.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, i32, vp]
+    L.ep_moe_create.argtypes = [c.POINTER(ep_moe_cfg_t), c.POINTER(vp)]
+    L.ep_moe_forward.argtypes = [vp, vp, i32, vp, vp, mw, vp, vp, i32, vp]
+    L.ep_moe_layer.argtypes = [vp, rc, vp, i32, vp, i32, i64, vp, mw, vp, vp, vp, vp, i32, vp]
+    L.ep_moe_status.argtypes = [vp, c.POINTER(i32)]
+    L.ep_moe_free.argtypes = [vp]
+    L.ep_moe_free.restype = None
+    for f in (L.ep_route, L.ep_route_backward, L.ep_w4_linear, L.ep_moe_create, L.ep_moe_forward,
+              L.ep_moe_layer, L.ep_moe_status):
+        f.restype = c.c_int
+    _lib = L
+    return L
+
+
+def _is(t, dtype, shape):
+    return t.dtype == dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
+# ------------------------------------------------------------------ router
+
+def make_route_cfg(num_experts, topk, score="softmax", renormalize=True, scale=1.0):
+    s = _SCORES[score] if isinstance(score, str) else int(score)
+    return ep_route_cfg_t(num_experts, topk, s, int(bool(renormalize)), scale)
+
+
+def _logits(cfg, logits, what):
+    _require(logits.is_cuda and logits.dim() == 2 and logits.shape[1] == cfg.num_experts and
+             logits.dtype in _FLOATS, "%s must be a bf16 or fp32 CUDA tensor [n, num_experts]" % what)
+    _require(logits.stride(1) == 1 or logits.shape[1] == 1 or logits.shape[0] == 0,
+             "%s must have contiguous rows" % what)
+    # a single row may carry any stride; rows may not overlap
+    return logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), cfg.num_experts)
+
+
+def _route_args(cfg, logits, topk_idx, topk_weights, select_bias):
+    stride = _logits(cfg, logits, "logits")
+    shape = (logits.shape[0], cfg.topk)
+    _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
+    _require(_is(topk_weights, torch.float32, shape),
+             "topk_weights must be a contiguous fp32 CUDA tensor [n, topk]")
+    _require(select_bias is None or _is(select_bias, torch.float32, (cfg.num_experts,)),
+             "select_bias must be a contiguous fp32 CUDA tensor [num_experts]")
+    return stride
+
+
+def ep_route(cfg, logits, topk_idx, topk_weights, select_bias=None, stream=None):
+    """Scores [n, E] (bf16 or fp32, contiguous rows at any row stride) to the
+    topk_idx (int64) and topk_weights (fp32) [n, K] that layout and combine take."""
+    stride = _route_args(cfg, logits, topk_idx, topk_weights, select_bias)
+    _check(_load().ep_route(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride, _ptr(select_bias),
+                            logits.shape[0], topk_idx.data_ptr(), topk_weights.data_ptr(),
+                            _stream_ptr(stream, logits.device)))
+
+
+def ep_route_backward(cfg, logits, topk_idx, grad_weights, grad_logits, stream=None):
+    """Gradient of ep_route's topk_weights: grad_weights fp32 [n, K] in,
+    grad_logits [n, E] of the logits' type out (every element written)."""
+    stride = _logits(cfg, logits, "logits")
+    gstride = _logits(cfg, grad_logits, "grad_logits")
+    _require(grad_logits.dtype == logits.dtype and grad_logits.shape == logits.shape,
+             "grad_logits must have the type and shape of logits")
+    shape = (logits.shape[0], cfg.topk)
+    _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
+    _require(_is(grad_weights, torch.float32, shape),
+             "grad_weights must be a contiguous fp32 CUDA tensor [n, topk]")
+    _check(_load().ep_route_backward(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride,
+                                     topk_idx.data_ptr(), grad_weights.data_ptr(), logits.shape[0],
+                                     grad_logits.data_ptr(), gstride, _stream_ptr(stream, logits.device)))
+
+
+# ----------------------------------------------------------- 4-bit weights
+
+def ep_w4_linear(x, qweight, scales, out, stream=None):
+    """out[n, rows] = x[n, cols] . W^T for up to 64 tokens.  qweight: uint8
+    [rows, cols/2] (low nibble: the even column, value nibble - 8); scales: fp32
+    [rows, cols/group] with group 32, 64 or 128; x bf16, out bf16 or fp32."""
+    _require(x.dim() == 2 and qweight.dim() == 2 and scales.dim() == 2, "x, qweight and scales must be 2-D")
+    n, cols = x.shape
+    rows, groups = scales.shape
+    _require(_is(x, torch.bfloat16, (n, cols)), "x must be a contiguous bf16 CUDA tensor [n, cols]")
+    _require(cols % 2 == 0 and _is(qweight, torch.uint8, (rows, cols // 2)),
+             "qweight must be a contiguous uint8 CUDA tensor [rows, cols / 2]")
+    _require(groups > 0 and cols % groups == 0 and _is(scales, torch.float32, (rows, groups)),
+             "scales must be a contiguous fp32 CUDA tensor [rows, cols / group_size]")
+    _require(out.dtype in _FLOATS and _is(out, out.dtype, (n, rows)),
+             "out must be a contiguous bf16 or fp32 CUDA tensor [n, rows]")
+    _check(_load().ep_w4_linear(x.data_ptr(), n, qweight.data_ptr(), scales.data_ptr(), rows, cols,
+                                cols // groups, out.data_ptr(), _FLOATS[out.dtype],
+                                _stream_ptr(stream, x.device)))
+
+
+# --------------------------------------------- MoE layer for a few tokens
+
+def make_moe_cfg(hidden_dim, intermediate_dim, num_experts, num_expert_per_token,
+                 max_tokens=EP_FEW_TOKENS, weight_dtype="bf16", group_size=0, activation="silu"):
+    wd = _WEIGHTS[weight_dtype] if isinstance(weight_dtype, str) else int(weight_dtype)
+    act = _ACTS[activation] if isinstance(activation, str) else int(activation)
+    return ep_moe_cfg_t(hidden_dim, intermediate_dim, num_experts, num_expert_per_token, max_tokens,
+                        wd, group_size, act)
+
+
+class EpMoeWeights:
+    """The experts' weights: w13 [E, 2I, H] (gate rows, then up rows) and w2
+    [E, H, I], both bf16, or both uint8 of the 4-bit form with fp32 scales
+    [E, 2I, H/group] and [E, H, I/group].  Keeps the tensors alive."""
+
+    def __init__(self, w13, w2, w13_scales=None, w2_scales=None):
+        self.tensors = (w13, w2, w13_scales, w2_scales)
+        for t in self.tensors:
+            _require(t is None or (t.is_cuda and t.is_contiguous() and t.dim() == 3),
+                     "weights and scales must be contiguous 3-D CUDA tensors")
+        _require((w13_scales is None) == (w2_scales is None),
+                 "w13_scales and w2_scales come together")
+        q = w13_scales is not None
+        _require(w13.dtype == w2.dtype == (torch.uint8 if q else torch.bfloat16),
+                 "w13 and w2 must be bf16, or uint8 with scales")
+        _require(not q or w13_scales.dtype == w2_scales.dtype == torch.float32, "scales must be fp32")
+        self.int4 = q
+        self.c = ep_moe_weights_t(w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(), _ptr(w2_scales))
+        self._fits = None
+
+    def check(self, cfg):
+        """Raise unless the shapes are those of cfg (looked at once per configuration object)."""
+        if self._fits is cfg:
+            return
+        E, H, I, g = cfg.num_experts, cfg.hidden_dim, cfg.intermediate_dim, cfg.group_size
+        _require(self.int4 == (cfg.weight_dtype == EP_INT4X2), "weights are not of the handle's weight_dtype")
+        per = 2 if self.int4 else 1
+        want = [(E, 2 * I, H // per), (E, H, I // per)]
+        want += [(E, 2 * I, H // g), (E, H, I // g)] if self.int4 else []
+        for t, s in zip(self.tensors, want):
+            _require(tuple(t.shape) == s, "weights have shape %s, expected %s" % (tuple(t.shape), s))
+        self._fits = cfg
+
+
+class EpMoe:
+    """Owner of an ep_moe_t: the experts of a few tokens (forward), or the whole
+    layer with its router (layer).  Equal inputs give equal bits."""
+
+    def __init__(self, cfg):
+        self.cfg = cfg
+        self._m = None
+        self.device = torch.cuda.current_device()
+        m = ctypes.c_void_p()
+        _check(_load().ep_moe_create(ctypes.byref(cfg), ctypes.byref(m)))
+        self._m = m
+
+    @property
+    def ptr(self):
+        if self._m is None:
+            raise EpError(EP_EINVAL, "handle already freed")
+        return self._m
+
+    def _args(self, x, weights, topk_idx, topk_weights, out, bias):
+        n, cfg = x.shape[0], self.cfg
+        _require(_is(x, torch.bfloat16, (n, cfg.hidden_dim)), "x must be a contiguous bf16 CUDA tensor [n, hidden]")
+        shape = (n, cfg.num_expert_per_token)
+        _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
+        _require(_is(topk_weights, torch.float32, shape),
+                 "topk_weights must be a contiguous fp32 CUDA tensor [n, topk]")
+        _require(out.dtype in _FLOATS and _is(out, out.dtype, x.shape),
+                 "out must be a contiguous bf16 or fp32 CUDA tensor [n, hidden]")
+        _require(bias is None or _is(bias, torch.bfloat16, x.shape),
+                 "bias must be a contiguous bf16 CUDA tensor [n, hidden]")
+        weights.check(cfg)
+        return n
+
+    def forward(self, x, topk_idx, topk_weights, weights, out, bias=None, stream=None):
+        """out[t] = sum_k topk_weights[t,k] * W2[e] (act(W1[e] x[t]) * W3[e] x[t]) (+ bias[t])."""
+        n = self._args(x, weights, topk_idx, topk_weights, out, bias)
+        _check(_load().ep_moe_forward(self.ptr, x.data_ptr(), n, topk_idx.data_ptr(),
+                                      topk_weights.data_ptr(), weights.c, _ptr(bias), out.data_ptr(),
+                                      _FLOATS[out.dtype], _stream_ptr(stream, self.device)))
+
+    def layer(self, route_cfg, x, logits, weights, topk_idx, topk_weights, out, bias=None,
+              select_bias=None, stream=None):
+        """ep_route of logits into topk_idx and topk_weights, then forward with them."""
+        n = self._args(x, weights, topk_idx, topk_weights, out, bias)
+        stride = _logits(route_cfg, logits, "logits")
+        _require(logits.shape[0] == n, "logits must have a row for each row of x")
+        _require(select_bias is None or _is(select_bias, torch.float32, (route_cfg.num_experts,)),
+                 "select_bias must be a contiguous fp32 CUDA tensor [num_experts]")
+        _check(_load().ep_moe_layer(self.ptr, route_cfg, x.data_ptr(), n, logits.data_ptr(),
+                                    _FLOATS[logits.dtype], stride, _ptr(select_bias), weights.c,
+                                    _ptr(bias), topk_idx.data_ptr(), topk_weights.data_ptr(),
+                                    out.data_ptr(), _FLOATS[out.dtype], _stream_ptr(stream, self.device)))
+
+    def status(self):
+        v = ctypes.c_int32()
+        _check(_load().ep_moe_status(self.ptr, ctypes.byref(v)))
+        return v.value
+
+    def free(self):
+        if self._m is not None:
+            _load().ep_moe_free(self._m)
+            self._m = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass

@@ -34,7 +34,7 @@ def sources():
 def _digest():
     h = hashlib.sha256()
     for f in sorted(sources() + glob.glob(os.path.join(CSRC, "*.h*")) +
-                    glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "ep_gb300.h")]):
+                    glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))):
         h.update(os.path.relpath(f, ROOT).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
