@@ -135,7 +135,7 @@ struct ep_moe {
   void* block = nullptr;
   void* h = nullptr;
   float* part = nullptr;
-  int32_t* err = nullptr;
+  int32_t *ready = nullptr, *tile_done = nullptr, *blocks_done = nullptr, *err = nullptr;
   uint64_t wait_ns = 0;
 };
 
@@ -182,6 +182,9 @@ int check_forward(ep_moe_t m, const void* x, int32_t n, const int64_t* idx, cons
   p->out_f32 = out_dtype == EP_FP32;
   p->h = m->h;
   p->part = m->part;
+  p->ready = m->ready;
+  p->tile_done = m->tile_done;
+  p->blocks_done = m->blocks_done;
   p->err = m->err;
   p->wait_ns = m->wait_ns;
   return EP_OK;
@@ -277,9 +280,10 @@ int ep_moe_create(const ep_moe_cfg_t* cfg, ep_moe_t* out) noexcept {
     m->wait_ns = WaitLimitNs();
     const size_t entries = static_cast<size_t>(cfg->max_tokens) * cfg->num_expert_per_token;
     auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
-    const size_t n_h = up(entries * cfg->intermediate_dim * 2);
+    const size_t n_h = up(entries * cfg->intermediate_dim * 4);
     const size_t n_part = up(entries * cfg->hidden_dim * sizeof(float));
-    const size_t total = n_h + n_part + up(sizeof(int32_t));
+    const size_t n_tile = static_cast<size_t>(cfg->hidden_dim + 15) / 16;
+    const size_t total = n_h + n_part + up(sizeof(int32_t) * (entries + n_tile + 2));
     if ((e = cudaStreamCreateWithFlags(&m->own_stream, cudaStreamNonBlocking)) != cudaSuccess)
       return bail(fail_cuda(e, "cudaStreamCreateWithFlags"));
     if ((e = cudaMallocAsync(&m->block, total, m->own_stream)) != cudaSuccess) {
@@ -291,7 +295,10 @@ int ep_moe_create(const ep_moe_cfg_t* cfg, ep_moe_t* out) noexcept {
     char* b = static_cast<char*>(m->block);
     m->h = b;
     m->part = reinterpret_cast<float*>(b + n_h);
-    m->err = reinterpret_cast<int32_t*>(b + n_h + n_part);
+    m->ready = reinterpret_cast<int32_t*>(b + n_h + n_part);
+    m->tile_done = m->ready + entries;
+    m->blocks_done = m->tile_done + n_tile;
+    m->err = m->blocks_done + 1;
     if ((e = cudaMemsetAsync(m->block, 0, total, m->own_stream)) != cudaSuccess)
       return bail(fail_cuda(e, "cudaMemsetAsync"));
     if ((e = cudaStreamSynchronize(m->own_stream)) != cudaSuccess)

@@ -56,8 +56,12 @@ struct MoeParams {
   int act;
   bool out_f32;
   // workspace
-  void* h;                  // bf16 [max_tokens * K, I]
+  void* h;                  // bf16 [max_tokens * K, 2, I]: the upper and the lower half of h
   float* part;              // [max_tokens * K, H]
+  // counters, zero between launches
+  int32_t* ready;           // [min(E, max_tokens * K)] finished gate/up items by active expert
+  int32_t* tile_done;       // [H / 16] finished down items by channel tile
+  int32_t* blocks_done;     // [1]
   int32_t* err;
   uint64_t wait_ns;
 };
