@@ -3,13 +3,17 @@
 //
 // What bounds it: every active expert's 3 H I weights are read once (a token's
 // own rows are a few KB), so the work is to keep HBM busy from the first byte to
-// the last.  A persistent grid, one block of 8 warps per SM, walks one list of
-// items: first the gate/up items (expert, 16 or 32 channels: the gate's and the
-// up projection's rows together, so that the product act(gate) up is formed where
-// the sums are), then the down items (expert, 32 or 64 output channels).  The 8
-// warps split an item's k range chunk by chunk and add their sums through shared
-// memory; each warp streams its own chunks through its own cp.async ring
-// (ep_stream.cuh) across items and phases, so the ring never drains.
+// the last.  A persistent grid, one block per SM, walks one list of
+// items: first the gate/up items (expert, 16 or more channels: the gate's and the up
+// projection's rows together, so that the product act(gate) up is formed where
+// the sums are), then the down items (expert, 32 or more output channels).  Eight
+// warps split an item's k range chunk by chunk; each streams its own chunks through
+// its own cp.async ring (ep_stream.cuh) across items and phases, so the ring never
+// drains.  For each column tile of an item (a round) they leave their sums in one
+// of two buffers and go on; two more warps, one for each buffer, add up the
+// sums and write the round's results; one last warp tells the other blocks, with
+// one memory fence for all the rounds written since its last one.  So neither the
+// sums nor the microseconds of a fence and an atomic stop the streams.
 //
 // A down item needs its expert's whole h: a counter per active expert, raised by
 // each finished gate/up item, is waited for (bounded) just before the item's
@@ -20,9 +24,10 @@
 // down product whose sums are added: a column costs nothing until 4 tokens meet
 // on an expert, and the rounding of h to 8 bits would double the output's error.
 //
-// The down items write fp32 expert rows; the block that finishes the last item of
+// The down items write fp32 expert rows; the block that finishes the last round of
 // a channel tile folds the K rows of each token in order (fmaf over k, as the
-// combine does).  No sum depends on the order of blocks: equal inputs, equal bits.
+// combine does) once its own items are done.  No sum depends on the order of
+// blocks: equal inputs, equal bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,6 +35,7 @@
 
 #include "ep_moe_kernels.hpp"
 #include "ep_stream.cuh"
+#include "ep_tma.cuh"
 #include "ep_types.cuh"
 
 namespace epg {
@@ -37,15 +43,10 @@ namespace {
 
 using stream::Form;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-
-// Row tiles of an item: bf16 32 rows, 4-bit 64.
-template <int G>
-using MoeForm = Form<G, G == 0 ? 2 : 4>;
-
+constexpr int kFinishers = 2;             // warps that finish rounds, one buffer each
+constexpr int kMaxEntries = kFewTokens * 16;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kSmemLimit = 232448 - 256;  // dynamic shared memory of one block (its static part aside)
+constexpr int kSmemLimit = 232448 - 3072;  // dynamic shared memory of one block (its static part aside)
 
 __device__ __forceinline__ float activate(float g, int act) {
   if (act == 0) return g / (1.0f + expf(-g));
@@ -65,65 +66,125 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-// A job: some tokens (at most the phase's cap) of one active expert.
+// Named barrier kBarFull + b: the streaming warps' sums of a round are in buffer b.
+// They arrive, the buffer's finishing warp waits.
+constexpr int kBarFull = 1;
+template <int THREADS>
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
+
+// Rounds written whose word to the other blocks may be outstanding; a power of two.
+constexpr int kQueue = 64;
+
+// Where the sum of a row and a column (8 of them) or a token (4) lies: both the
+// writing lanes (fragments) and the reading ones (rows in sequence) miss each
+// other's banks.
+__device__ __forceinline__ int red_8(int row, int col) { return row * 8 + (col ^ (row >> 1 & 6)); }
+__device__ __forceinline__ int red_4(int row, int tok) { return row * 4 + (tok ^ (row >> 3 & 3)); }
+
+// Until *count >= want, a count in shared memory that another warp raises; gives
+// up (false) after the clean-up limit.
+__device__ __forceinline__ bool await_count(const int* count, int want) {
+  const volatile int* c = count;
+  if (*c >= want) return true;
+  const uint64_t t0 = now_ns();
+  while (*c < want) {
+    if (now_ns() - t0 > tma::kDrainNs) return false;
+    __nanosleep(64);
+  }
+  return true;
+}
+
+// A job: some tokens (at most the phase's cap, 16) of one active expert, in one
+// word: the expert, the first of its entries in the grouped list, how many, and
+// the column tiles of 8 tokens that the whole expert has.
 struct Job {
-  uint16_t expert, active, start, count;
+  int expert, start, count, parts;
 };
+__device__ __forceinline__ uint32_t pack_job(int expert, int start, int count, int parts) {
+  return static_cast<uint32_t>(expert) | static_cast<uint32_t>(start) << 11 | static_cast<uint32_t>(count - 1) << 21 |
+         static_cast<uint32_t>(parts - 1) << 25;
+}
+__device__ __forceinline__ Job unpack_job(uint32_t j) {
+  return {static_cast<int>(j & 2047), static_cast<int>(j >> 11 & 1023), static_cast<int>(j >> 21 & 15) + 1,
+          static_cast<int>(j >> 25) + 1};
+}
 
 // Shared memory behind the rings, sized by the number of entries n K.
 struct Lists {
-  Job *jobs_0, *jobs_1;
-  float* weight;       // by entry
+  uint32_t *jobs_0, *jobs_1;
   uint16_t* entry;     // entries grouped by expert, ascending within one
-  uint16_t* token;     // entry / K
-  uint16_t* parts;     // by active expert: its gate/up jobs
-  uint8_t* valid;      // by entry
+  uint32_t* valid;     // by entry, one bit each
 };
 
-constexpr int lists_bytes(int entries) { return ((entries * (2 * 8 + 4 + 3 * 2 + 1) + 15) & ~15) + 16; }
+constexpr int lists_bytes(int entries) { return (entries * (4 + 4 + 2) + entries / 8 + 4 + 15) & ~15; }
+// Channel tiles of the down product that one block may have to fold: at most
+// every tile (hidden_dim <= 32768 over 32 channels).
+constexpr int kMaxTiles = 1024;
 
+// How a block is cut for weights of form G and up to NT column tiles a job.  The
+// ring takes what shared memory is left; 64 KB of weights under way per SM carry
+// HBM's full rate.
 template <int G, int NT>
 struct Shape {
-  using F = MoeForm<G>;
+  // 4 row tiles spare 4-bit weights half the work on the activations; with 16
+  // columns they would leave the ring too short
+  static constexpr int kRowTiles = G != 0 && NT == 1 ? 4 : 2;
+  static constexpr int kEnough = 8;                          // stages of a warp in an item (see widen)
+  using F = Form<G, kRowTiles>;
+  static constexpr int kWarps = 8;
+  static constexpr int kAllWarps = kWarps + kFinishers + 1;
+  static constexpr int kThreads = 32 * kAllWarps;
   static constexpr int kTokens = NT == 1 ? 8 : kFewTokens;   // most tokens of a call
-  static constexpr int kRed = kWarps * F::kRows * 10 * 4;    // partial sums of one column tile
+  static constexpr int kRed = kWarps * F::kRows * 8 * 4;     // one round's partial sums, one of two buffers
   static constexpr int kSlot = F::stage_bytes(NT);
-  static constexpr int kFit = (kSmemLimit - kRed - lists_bytes(kTokens * 16)) / (kWarps * kSlot);
+  static constexpr int kFit = (kSmemLimit - 2 * kRed - lists_bytes(kTokens * 16)) / (kWarps * kSlot);
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kRing = kWarps * kStages * kSlot;
-  static_assert(kStages >= 2);
+  static_assert(kStages >= 3 && 8 * NT <= 16);
   // the expert counts of the set-up (2048 x 4 bytes) and the ranks use the ring
-  static_assert(kRing >= 4 * 2048 + 2 * 1024 + 2 * 1024);
+  static_assert(kRing >= 4 * 2048 + 4 * kMaxEntries);
 };
 
 template <int G, int NT>
-__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
-  using F = MoeForm<G>;
+__global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const MoeParams p) {
   using S = Shape<G, NT>;
-  constexpr int RT = F::kRowTiles, kStages = S::kStages;
+  using F = typename S::F;
+  constexpr int RT = F::kRowTiles, kStages = S::kStages, kWarps = S::kWarps, kAllWarps = S::kAllWarps;
+  constexpr int kThreads = S::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t scan_warp[kWarps];
-  __shared__ int s_flag, s_lost;
+  __shared__ uint64_t scan_warp[kAllWarps];
+  __shared__ int s_flag, s_lost, s_rounds, s_finished;
+  __shared__ __align__(8) uint64_t s_free[2];
+  __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
+  __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
+  __shared__ uint16_t finished[kMaxTiles];   // the tiles this block folds
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int entries = p.n * p.topk;
-  float* red = reinterpret_cast<float*>(smem + S::kRing);
+  float* red_all = reinterpret_cast<float*>(smem + S::kRing);
   Lists L;
   {
-    uint8_t* b = smem + S::kRing + S::kRed;
-    L.jobs_0 = reinterpret_cast<Job*>(b);
+    uint8_t* b = smem + S::kRing + 2 * S::kRed;
+    L.jobs_0 = reinterpret_cast<uint32_t*>(b);
     L.jobs_1 = L.jobs_0 + entries;
-    L.weight = reinterpret_cast<float*>(L.jobs_1 + entries);
-    L.entry = reinterpret_cast<uint16_t*>(L.weight + entries);
-    L.token = L.entry + entries;
-    L.parts = L.token + entries;
-    L.valid = reinterpret_cast<uint8_t*>(L.parts + entries);
+    L.valid = L.jobs_1 + entries;
+    L.entry = reinterpret_cast<uint16_t*>(L.valid + (entries + 31) / 32);
   }
 
   // ---- which experts, with which tokens: every block works it out for itself
   int* count = reinterpret_cast<int*>(smem);                              // by expert
   uint16_t* expert_of = reinterpret_cast<uint16_t*>(smem + 4 * 2048);     // by entry
-  uint16_t* rank_of = expert_of + 1024;
-  if (tid == 0) s_lost = 0;
+  uint16_t* rank_of = expert_of + kMaxEntries;
+  if (tid == 0) {
+    s_lost = s_rounds = s_finished = s_written[0] = s_written[1] = s_told = 0;
+    for (int b = 0; b < 2; ++b) tma::mbar_init(stream::smem_addr(&s_free[b]), 1);
+  }
+  const uint32_t free_bar = stream::smem_addr(s_free);
   for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
   __syncthreads();
   if (warp == 0) {   // one warp in entry order: the order within an expert is the same in every block
@@ -135,30 +196,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
       if (i < entries && !ok && id != -1 && blockIdx.x == 0) atomicOr(p.err, kErrBadExpert);
       const int e = ok ? static_cast<int>(id) : -1 - lane;
       const unsigned same = __match_any_sync(kAll, e);
+      const unsigned oks = __ballot_sync(kAll, ok);
       const int before = ok ? count[e] : 0;
       __syncwarp();
       if (ok && (same >> lane) == 1u) count[e] = before + __popc(same);   // the last of the equal ones
       __syncwarp();
+      if (lane == 0) L.valid[i0 / 32] = oks;
       if (i < entries) {
         expert_of[i] = ok ? static_cast<uint16_t>(e) : 0xffff;
         rank_of[i] = static_cast<uint16_t>(before + __popc(same & ((1u << lane) - 1u)));
-        L.valid[i] = ok;
       }
     }
   }
   __syncthreads();
-  int jobs_0, jobs_1, actives;
+  int jobs_0, jobs_1;
   {
-    // four 16-bit sums in one word: entries, active experts, gate/up jobs, down jobs
+    // three 16-bit sums in one word: entries, gate/up jobs, down jobs
     const int per = (p.experts + kThreads - 1) / kThreads, e0 = tid * per;
     const int e1 = min(e0 + per, p.experts);
     auto word = [](int c) -> uint64_t {
       return c == 0 ? 0
-                    : static_cast<uint64_t>(c) | 1ull << 16 | static_cast<uint64_t>((c + 8 * NT - 1) / (8 * NT)) << 32 |
-                          static_cast<uint64_t>((c + 4 * NT - 1) / (4 * NT)) << 48;
+                    : static_cast<uint64_t>(c) | static_cast<uint64_t>((c + 8 * NT - 1) / (8 * NT)) << 16 |
+                          static_cast<uint64_t>((c + 4 * NT - 1) / (4 * NT)) << 32;
     };
     uint64_t mine = 0;
-    for (int e = e0; e < e1; ++e) mine += word(count[e]);
+    int rounds = 0;        // down rounds of one channel tile
+    for (int e = e0; e < e1; ++e) mine += word(count[e]), rounds += (count[e] + 3) >> 2;
+    if (rounds) atomicAdd(&s_rounds, rounds);
     uint64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -168,24 +232,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
     if (lane == 31) scan_warp[warp] = upto;
     __syncthreads();
     uint64_t base = upto - mine, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kAllWarps; ++w) {
       if (w < warp) base += scan_warp[w];
       all += scan_warp[w];
     }
-    actives = static_cast<int>(all >> 16 & 0xffff);
-    jobs_0 = static_cast<int>(all >> 32 & 0xffff);
-    jobs_1 = static_cast<int>(all >> 48);
+    jobs_0 = static_cast<int>(all >> 16 & 0xffff);
+    jobs_1 = static_cast<int>(all >> 32 & 0xffff);
     for (int e = e0; e < e1; ++e) {
       const int c = count[e];
       if (c == 0) continue;
-      const int start = static_cast<int>(base & 0xffff), active = static_cast<int>(base >> 16 & 0xffff);
+      const int start = static_cast<int>(base & 0xffff);
       for (int ph = 0; ph < 2; ++ph) {
         const int cap = ph == 0 ? 8 * NT : 4 * NT;
-        int j = static_cast<int>(base >> (32 + 16 * ph) & 0xffff);
-        if (ph == 0) L.parts[active] = static_cast<uint16_t>((c + cap - 1) / cap);
+        int j = static_cast<int>(base >> (16 + 16 * ph) & 0xffff);
         for (int o = 0; o < c; o += cap, ++j)
-          (ph == 0 ? L.jobs_0 : L.jobs_1)[j] = {static_cast<uint16_t>(e), static_cast<uint16_t>(active), static_cast<uint16_t>(start + o),
-                           static_cast<uint16_t>(min(cap, c - o))};
+          (ph == 0 ? L.jobs_0 : L.jobs_1)[j] = pack_job(e, start + o, min(cap, c - o), (c + 7) >> 3);
       }
       base += word(c);
       count[e] = start;
@@ -195,10 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
   for (int i = tid; i < entries; i += kThreads) {
     const int e = expert_of[i];
     if (e != 0xffff) {
-      const int at = count[e] + rank_of[i];
-      L.entry[at] = static_cast<uint16_t>(i);
-      L.token[at] = static_cast<uint16_t>(i / p.topk);
-      L.weight[i] = p.topk_weights[i];
+      L.entry[count[e] + rank_of[i]] = static_cast<uint16_t>(i);
     }
   }
   __syncthreads();   // the ring's memory is free from here on
@@ -207,90 +265,150 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
   // (pick: by phase, without arrays that would have to live in memory)
   auto pick = [](int ph, auto a, auto b) { return ph == 0 ? a : b; };
   auto dim_k = [&](int ph) { return pick(ph, p.hidden, p.inter); };       // columns of the weight rows
-  const int tiles_0 = (p.inter + F::kRows / 2 - 1) / (F::kRows / 2), tiles_1 = (p.hidden + F::kRows - 1) / F::kRows;
+  constexpr int kHalf = F::kRows / 2;       // gate rows, and up rows, of a gate/up tile
+  const int grid = gridDim.x;
+  const int chunks_0 = (p.hidden + F::kCols - 1) / F::kCols, chunks_1 = (p.inter + F::kCols - 1) / F::kCols;
+  auto chunks = [&](int ph) { return pick(ph, chunks_0, chunks_1); };
+  // An item is `wide` row tiles side by side, 1, 2 or 4, each with its share of the
+  // warps: where the columns are few, one tile would give a warp so few stages that
+  // setting them up costs more than they do.  As long as every block keeps enough
+  // items for all to end together.
+  auto widen = [&](int subtiles, int jobs, int n_chunks) {
+    int r = 1;
+    while (r < 4 && n_chunks * r < S::kEnough * kWarps && jobs * ((subtiles + 2 * r - 1) / (2 * r)) >= 12 * grid) r *= 2;
+    return r;
+  };
+  const int sub_0 = (p.inter + kHalf - 1) / kHalf, sub_1 = (p.hidden + F::kRows - 1) / F::kRows;
+  const int side_0 = widen(sub_0, jobs_0, chunks_0), side_1 = widen(sub_1, jobs_1, chunks_1);
+  auto side = [&](int ph) { return pick(ph, side_0, side_1); };
+  const int tiles_0 = (sub_0 + side_0 - 1) / side_0, tiles_1 = (sub_1 + side_1 - 1) / side_1;
   auto tiles = [&](int ph) { return pick(ph, tiles_0, tiles_1); };
   auto jobs_of = [&](int ph) { return pick(ph, jobs_0, jobs_1); };
-  auto job_at = [&](int ph, int j) { return pick(ph, L.jobs_0, L.jobs_1)[j]; };
-  const int grid = gridDim.x;
+  auto job_at = [&](int ph, int j) { return unpack_job(pick(ph, L.jobs_0, L.jobs_1)[j]); };
+  const uint32_t by_topk = 65536u / static_cast<uint32_t>(p.topk) + 1;    // entry / topk, exact below 2^14
   // this block's first item of each phase: the down items go on where the gate/up items ended
   const int first_1 = (static_cast<int>(blockIdx.x) - jobs_0 * tiles_0 % grid + grid) % grid;
   auto first = [&](int ph) { return pick(ph, static_cast<int>(blockIdx.x), first_1); };
-  const int chunks_0 = (p.hidden + F::kCols - 1) / F::kCols, chunks_1 = (p.inter + F::kCols - 1) / F::kCols;
-  auto chunks = [&](int ph) { return pick(ph, chunks_0, chunks_1); };
 
+  if (warp < kWarps) {   // ---- the streaming warps
   const uint32_t ring = stream::smem_addr(smem) + warp * kStages * S::kSlot;
-  const bool wide_0 = F::kInt4 && p.hidden % 128 == 0 && (reinterpret_cast<uintptr_t>(p.w13_scales) & 15) == 0;
-  const bool wide_1 = F::kInt4 && p.inter % 128 == 0 && (reinterpret_cast<uintptr_t>(p.w2_scales) & 15) == 0;
+  const bool whole_0 = F::kInt4 && p.hidden % 128 == 0 && (reinterpret_cast<uintptr_t>(p.w13_scales) & 15) == 0;
+  const bool whole_1 = F::kInt4 && p.inter % 128 == 0 && (reinterpret_cast<uintptr_t>(p.w2_scales) & 15) == 0;
 
-  // A walk: the chunk c of an item (job, tile) of a phase.
+  // This warp's place in an item: row tile `sub` of it, and chunk c = lead, lead +
+  // step, ... of the columns; an item's last chunk is followed by the next item's
+  // first, so that no warp has more chunks than another in the long run.
+  auto step = [&](int ph) { return kWarps / side(ph); };
+  auto sub = [&](int ph) { return warp / step(ph); };
+  auto lead = [&](int ph) { return warp % step(ph); };
   struct Walk {
     int ph, job, tile, c;
   };
-  auto settle = [&](Walk& w) {   // to a chunk that exists: over item ends, and phases without work for this warp
+  auto begin = [&](Walk& w, int ph) { w = {ph, 0, pick(ph, first(0), first(1)), ph < 2 ? lead(ph) : 0}; };
+  // to an item where this warp has a chunk: over the ends of items, jobs and phases
+  auto settle = [&](Walk& w) {
     while (w.ph < 2) {
       while (w.tile >= tiles(w.ph)) w.tile -= tiles(w.ph), ++w.job;
-      if (w.job < jobs_of(w.ph) && w.c < chunks(w.ph)) return;
-      ++w.ph;
-      if (w.ph < 2) w.job = 0, w.tile = first(w.ph), w.c = warp;
+      if (w.job >= jobs_of(w.ph)) {
+        begin(w, w.ph + 1);
+      } else if (w.c < chunks(w.ph)) {
+        return;
+      } else {
+        w.c -= chunks(w.ph);
+        w.tile += grid;
+      }
     }
   };
-  // the weights' part of a stage
-  uint32_t row_off[F::kCopies];   // of the rows this lane copies, in 16-byte units from the expert's matrix
+  // to the next chunk; true when that is another item
+  auto advance = [&](Walk& w) {
+    w.c += step(w.ph);
+    if (w.c < chunks(w.ph)) return false;
+    settle(w);
+    return true;
+  };
+
+  // What a lane copies of each stage of an item.  Weights: piece `lane_piece` of
+  // kCopies rows; activations: piece `lane_xpiece` of kXCopies columns; scales:
+  // of tile rows `lane`, `lane` + 32.
+  constexpr int kXCopies = 8 * NT * F::kXPieces / 32;
+  const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
+  const int lane_col = lane / F::kXPieces, lane_xpiece = lane % F::kXPieces;
+  const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
+  const uint8_t* w_src = nullptr;           // the expert's matrix, at this lane's piece
+  uint32_t row_off[F::kCopies];             // 16-byte units
+  const float* s_src[F::kRows / 32] = {};   // of tile rows `lane`, `lane` + 32
   auto channel_row = [&](int ph, int tile, int r) {
-    if (ph == 1) return min(tile * F::kRows + r, p.hidden - 1);
-    const int half = F::kRows / 2;
-    const int ch = min(tile * half + (r < half ? r : r - half), p.inter - 1);
-    return r < half ? ch : p.inter + ch;
+    const int at = tile * side(ph) + sub(ph);
+    if (ph == 1) return min(at * F::kRows + r, p.hidden - 1);
+    const int ch = min(at * kHalf + (r < kHalf ? r : r - kHalf), p.inter - 1);
+    return r < kHalf ? ch : p.inter + ch;
   };
-  auto enter_item = [&](const Walk& w) {
-    if (w.ph > 1) return;
-    const int pieces = dim_k(w.ph) / F::kPerPiece;
+  auto expert_scales = [&](const Walk& w) {
+    return pick(w.ph, p.w13_scales, p.w2_scales) +
+           static_cast<int64_t>(job_at(w.ph, w.job).expert) * pick(w.ph, 2 * p.inter, p.hidden) * (dim_k(w.ph) / (F::kInt4 ? G : 1));
+  };
+  auto enter_weights = [&](const Walk& w) {
+    const uint32_t pieces = dim_k(w.ph) / F::kPerPiece;
+    const int64_t rows = pick(w.ph, 2 * p.inter, p.hidden);
+    w_src = static_cast<const uint8_t*>(pick(w.ph, p.w13, p.w2)) +
+            (job_at(w.ph, w.job).expert * rows * pieces + lane_piece) * 16;
 #pragma unroll
-    for (int i = 0; i < F::kCopies; ++i) {
-      const int r = lane / F::kPieces + i * (32 / F::kPieces);
-      row_off[i] = static_cast<uint32_t>(channel_row(w.ph, w.tile, r)) * static_cast<uint32_t>(pieces);
+    for (int i = 0; i < F::kCopies; ++i)
+      row_off[i] = static_cast<uint32_t>(channel_row(w.ph, w.tile, lane_row + i * (32 / F::kPieces))) * pieces;
+    if constexpr (F::kInt4) {
+#pragma unroll
+      for (int i = 0; i < F::kRows / 32; ++i)
+        s_src[i] = expert_scales(w) + static_cast<int64_t>(channel_row(w.ph, w.tile, lane + 32 * i)) * (dim_k(w.ph) / G);
     }
   };
-  const uint32_t a_dst = F::a_offset(lane / F::kPieces, lane % F::kPieces);
   auto copy_weights = [&](const Walk& w, uint32_t slot) {
-    const int pieces = dim_k(w.ph) / F::kPerPiece;
-    const int64_t rows = w.ph == 0 ? 2 * p.inter : p.hidden;
-    const int e = job_at(w.ph, w.job).expert;
-    const uint8_t* base = static_cast<const uint8_t*>(w.ph == 0 ? p.w13 : p.w2) + e * rows * pieces * 16;
-    const int piece = w.c * F::kPieces + lane % F::kPieces;
-    const bool ok = piece < pieces;
-    const uint8_t* src = base + (ok ? piece * 16 : 0);
+    const bool ok = w.c * F::kPieces + lane_piece < dim_k(w.ph) / F::kPerPiece;
+    const uint8_t* src = w_src + (ok ? w.c * F::kRowBytes : 0);
 #pragma unroll
     for (int i = 0; i < F::kCopies; ++i)
       stream::copy16(slot + a_dst + i * (32 / F::kPieces) * F::kRowBytes, src + static_cast<uint64_t>(row_off[i]) * 16, ok);
     if constexpr (F::kInt4) {
-      const float* sc = (w.ph == 0 ? p.w13_scales : p.w2_scales) + e * rows * (dim_k(w.ph) / G);
-      stream::copy_scales<G, RT>(slot, lane, sc, dim_k(w.ph), w.c, pick(w.ph, wide_0, wide_1),
-                             [&](int r) { return channel_row(w.ph, w.tile, r); });
+      if (pick(w.ph, whole_0, whole_1)) {
+#pragma unroll
+        for (int i = 0; i < F::kRows / 32; ++i)
+          stream::copy_wide<4 * F::kScales>(slot + F::kABytes + 4 * F::kScales * (lane + 32 * i), s_src[i] + w.c * F::kScales);
+      } else {
+        stream::copy_scales<G, RT>(slot, lane, expert_scales(w), dim_k(w.ph), w.c,
+                                   [&](int r) { return channel_row(w.ph, w.tile, r); });
+      }
     }
   };
   // the activations' part: the job's columns (phase 1: the hi and the lo row of each entry)
-  auto copy_columns = [&](const Walk& w, uint32_t slot) {
+  uint32_t x_off[kXCopies];                 // elements, from x or h
+  int x_cols = 0;
+  auto enter_columns = [&](const Walk& w) {
     const Job job = job_at(w.ph, w.job);
-    const int k = dim_k(w.ph);
-    const int cols = w.ph == 0 ? job.count : 2 * job.count;
-    for (int q = lane; q < cols * F::kXPieces; q += 32) {
-      const int col = q / F::kXPieces, c = q % F::kXPieces;
-      const int at = w.c * F::kCols + 8 * c;
-      const __nv_bfloat16* src =
-          w.ph == 0 ? static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(L.token[job.start + col]) * k
-                    : static_cast<const __nv_bfloat16*>(p.h) +
-                          (2 * static_cast<int64_t>(L.entry[job.start + (col >> 1)]) + (col & 1)) * k;
-      stream::copy16(slot + F::x_offset(col, c), src + (at < k ? at : 0), at < k);
+    x_cols = pick(w.ph, 1, 2) * job.count;
+#pragma unroll
+    for (int i = 0; i < kXCopies; ++i) {
+      const int col = lane_col + i * (32 / F::kXPieces);
+      if (col < x_cols)
+        x_off[i] = (w.ph == 0 ? (L.entry[job.start + col] * by_topk >> 16) : 2u * L.entry[job.start + (col >> 1)] + static_cast<uint32_t>(col & 1)) *
+                   static_cast<uint32_t>(dim_k(w.ph));
+    }
+  };
+  auto copy_columns = [&](const Walk& w, uint32_t slot) {
+    const int at = w.c * F::kCols + 8 * lane_xpiece;
+    const bool ok = at < dim_k(w.ph);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(pick(w.ph, p.x, static_cast<const void*>(p.h))) + (ok ? at : 0);
+#pragma unroll
+    for (int i = 0; i < kXCopies; ++i) {
+      const int col = lane_col + i * (32 / F::kXPieces);
+      if (col < x_cols) stream::copy16(slot + F::x_offset(col, lane_xpiece), src + x_off[i], ok);
     }
   };
   // until every gate/up item of the job's expert is done; gives up after wait_ns
   auto await_expert = [&](const Walk& w) {
     const Job job = job_at(1, w.job);
-    const int want = tiles_0 * L.parts[job.active];
-    if (lane == 0 && load_acquire(p.ready + job.active) < want && !*static_cast<volatile int*>(&s_lost)) {
+    const int want = tiles_0 * job.parts;
+    if (lane == 0 && load_acquire(p.ready + job.expert) < want && !*static_cast<volatile int*>(&s_lost)) {
       const uint64_t t0 = now_ns();
-      while (load_acquire(p.ready + job.active) < want) {
+      while (load_acquire(p.ready + job.expert) < want) {
         if (now_ns() - t0 > p.wait_ns) {
           *static_cast<volatile int*>(&s_lost) = 1;
           atomicOr(p.err, kErrTimeout);
@@ -301,51 +419,56 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
     __syncwarp();
   };
 
-  Walk pf{0, 0, first(0), warp};
+  Walk pf;
+  begin(pf, 0);
   settle(pf);
-  enter_item(pf);
   int ahead = 0;           // stages of phase 1 whose weights are under way without their columns
   int phase = 0, awaited = -1;
+  bool fresh = true;       // pf stands at an item whose copies are not set up
   auto issue = [&](int slot_index) {
     if (pf.ph < 2) {
       const uint32_t slot = ring + slot_index * S::kSlot;
+      if (fresh) enter_weights(pf);
       copy_weights(pf, slot);
       if (pf.ph == phase) {
-        if (phase == 1 && pf.job != awaited) await_expert(pf), awaited = pf.job;
+        if (fresh) {
+          if (phase == 1 && pf.job != awaited) await_expert(pf), awaited = pf.job;
+          enter_columns(pf);
+        }
         copy_columns(pf, slot);
       } else {
         ++ahead;
       }
-      const int ph = pf.ph, job = pf.job, tile = pf.tile;
-      pf.c += kWarps;
-      if (pf.c >= chunks(ph)) pf.c = warp, pf.tile += grid;
-      settle(pf);
-      if (pf.ph != ph || pf.job != job || pf.tile != tile) enter_item(pf);
+      fresh = advance(pf);
     }
     stream::commit();
   };
+  int round = 0;
   int in = 0, out = 0;     // ring positions of the next stage to fill and to use
   for (int s = 0; s < kStages - 1; ++s) issue(in), ++in;
 
   for (phase = 0; phase < 2; ++phase) {
     if (phase == 1 && ahead > 0) {
-      Walk w{1, 0, first(1), warp};
+      Walk w;
+      begin(w, 1);
       settle(w);
       int slot = out;
+      bool enter = true;
       for (int s = 0; s < ahead; ++s) {
-        if (w.job != awaited) await_expert(w), awaited = w.job;
+        if (enter) {
+          if (w.job != awaited) await_expert(w), awaited = w.job;
+          enter_columns(w);
+        }
         copy_columns(w, ring + slot * S::kSlot);
         slot = slot + 1 == kStages ? 0 : slot + 1;
-        w.c += kWarps;
-        if (w.c >= chunks_1) w.c = warp, w.tile += grid;
-        settle(w);
+        enter = advance(w);
       }
+      // pf stands where w does; its item's columns are the ones just set up unless it is another item
       stream::commit();
       stream::wait<0>();
       __syncwarp();
     }
-    const int mine = warp < chunks(phase) ? (chunks(phase) - warp + kWarps - 1) / kWarps : 0;
-    int job_i = 0, tile = first(phase);
+    int job_i = 0, tile = first(phase), c = lead(phase);
     for (;; tile += grid) {
       while (tile >= tiles(phase)) tile -= tiles(phase), ++job_i;
       if (job_i >= jobs_of(phase)) break;
@@ -359,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
-      for (int j = 0; j < mine; ++j) {
+      for (; c < chunks(phase); c += step(phase)) {
         stream::wait<kStages - 2>();
         __syncwarp();      // every lane's copies of this stage, and every lane done with the slot refilled next
         issue(in);
@@ -368,96 +491,161 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
         out = out + 1 == kStages ? 0 : out + 1;
         if (NT == 1 || nts == 1)
           stream::consume<G, RT, 1, NT>(slot, lane, acc);
-        else if (NT == 2 || nts == 2)
-          stream::consume<G, RT, NT < 2 ? NT : 2, NT>(slot, lane, acc);
         else
           stream::consume<G, RT, NT, NT>(slot, lane, acc);
       }
-      // the warps' sums, one column tile at a time
+      c -= chunks(phase);
+      // one round per column tile: the sums to its buffer
       const int g = lane >> 2, t = lane & 3;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt >= nts) break;
+        const int buf = round & 1;
+        float* red = red_all + buf * (S::kRed / 4);
+        if (round >= 2 && !tma::mbar_wait_bounded(free_bar + 8 * buf, (round >> 1) - 1 & 1, tma::kDrainNs) && lane == 0)
+          atomicOr(p.err, kErrTimeout);
         if (phase == 0) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            float* r0 = red + (warp * F::kRows + 16 * rt + g) * 10 + 2 * t;
-            *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
-            *reinterpret_cast<float2*>(r0 + 80) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
-          }
-          __syncthreads();
-          constexpr int kCh = F::kRows / 2;
-          const int ch = tid % kCh, col = tid / kCh;
-          const int i = tile * kCh + ch;
-          if (col < 8 && 8 * nt + col < cols && i < p.inter) {
-            float gate = 0.0f, up = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              gate += red[(w * F::kRows + ch) * 10 + col];
-              up += red[(w * F::kRows + kCh + ch) * 10 + col];
-            }
-            const float h = activate(gate, p.act) * up;
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-            // an infinite or NaN h has nothing below it
-            const float rest = h - __bfloat162float(hi);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(rest == rest && fabsf(rest) < INFINITY ? rest : 0.0f);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.h) +
-                                 2 * static_cast<int64_t>(L.entry[job.start + 8 * nt + col]) * p.inter + i;
-            dst[0] = hi;
-            dst[p.inter] = lo;
+            float* r0 = red + warp * F::kRows * 8;
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g, 2 * t)) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g + 8, 2 * t)) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
           }
         } else {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            float* r0 = red + (warp * F::kRows + 16 * rt + g) * 4 + t;
-            r0[0] = acc[rt][nt][0] + acc[rt][nt][1];
-            r0[32] = acc[rt][nt][2] + acc[rt][nt][3];
-          }
-          __syncthreads();
-          const int r = tid % F::kRows, tok = tid / F::kRows;
-          const int c = tile * F::kRows + r;
-          if (tok < 4 && 4 * nt + tok < job.count && c < p.hidden) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += red[(w * F::kRows + r) * 4 + tok];
-            p.part[static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.hidden + c] = v;
+            float* r0 = red + warp * F::kRows * 4;
+            r0[red_4(16 * rt + g, t)] = acc[rt][nt][0] + acc[rt][nt][1];
+            r0[red_4(16 * rt + g + 8, t)] = acc[rt][nt][2] + acc[rt][nt][3];
           }
         }
-        __syncthreads();   // the sums' memory is free, the results are written
+        bar_arrive<32 * (kWarps + 1)>(kBarFull + buf);
+        ++round;
       }
-      if (phase == 0) {
-        if (tid == 0) {
-          __threadfence();
-          atomicAdd(p.ready + job.active, 1);
-        }
+    }
+  }
+  stream::wait<0>();
+  } else if (warp < kWarps + kFinishers) {
+    // ---- the finishing warps: every other round each
+    const int buf = warp - kWarps;
+    const float* red = red_all + buf * (S::kRed / 4);
+    int round = 0;
+    // the sums of the warps that share a row tile, in the order of warps
+    auto add_up = [](const float* at, int stride, int warps) {
+      float sum = 0.0f;
+      if (warps == kWarps) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += at[w * stride];
       } else {
-        if (tid == 0) {
-          __threadfence();
-          s_flag = atomicAdd(p.tile_done + tile, 1) == jobs_1 - 1;
-          __threadfence();
-        }
-        __syncthreads();
-        if (s_flag) {      // the tile's last item: fold every token's K rows
-          constexpr int kTok = kThreads / F::kRows;
-          const int c = tile * F::kRows + tid % F::kRows;
-          if (c < p.hidden) {
-            for (int tok = tid / F::kRows; tok < p.n; tok += kTok) {
-              float sum = 0.0f;
-              for (int k = 0; k < p.topk; ++k) {
-                const int en = tok * p.topk + k;
-                if (L.valid[en])
-                  sum = fmaf(L.weight[en], __ldcg(p.part + static_cast<int64_t>(en) * p.hidden + c), sum);
+        for (int w = 0; w < warps; ++w) sum += at[w * stride];
+      }
+      return sum;
+    };
+    for (int phase = 0; phase < 2; ++phase) {
+      const int step = kWarps / side(phase);
+      int job_i = 0, tile = first(phase);
+      for (;; tile += grid) {
+        while (tile >= tiles(phase)) tile -= tiles(phase), ++job_i;
+        if (job_i >= jobs_of(phase)) break;
+        const Job job = job_at(phase, job_i);
+        const int cols = pick(phase, 1, 2) * job.count;
+        for (int nt = 0; 8 * nt < cols; ++nt, ++round) {
+          if ((round & 1) != buf) continue;
+          bar_sync<32 * (kWarps + 1)>(kBarFull + buf);
+          if (phase == 0) {
+            const int n_cols = min(8, cols - 8 * nt);
+            for (int v = lane; v < side_0 * kHalf * n_cols; v += 32) {
+              const int ch = v % kHalf, at = v / kHalf % side_0, col = v / (kHalf * side_0);
+              const int i = (tile * side_0 + at) * kHalf + ch;
+              const float* from = red + at * step * F::kRows * 8;
+              const float gate = add_up(from + red_8(ch, col), F::kRows * 8, step);
+              const float up = add_up(from + red_8(kHalf + ch, col), F::kRows * 8, step);
+              if (i < p.inter) {
+                const float h = activate(gate, p.act) * up;
+                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                // an infinite or NaN h has nothing below it
+                const float rest = h - __bfloat162float(hi);
+                const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.h) +
+                                     2 * static_cast<int64_t>(L.entry[job.start + 8 * nt + col]) * p.inter + i;
+                dst[0] = hi;
+                dst[p.inter] = lo;
               }
-              const int64_t o = static_cast<int64_t>(tok) * p.hidden + c;
-              if (p.bias) sum += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[o]);
-              if (p.out_f32)
-                static_cast<float*>(p.out)[o] = sum;
-              else
-                static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum);
+            }
+          } else {
+            const int n_tok = min(4, job.count - 4 * nt);
+            for (int v = lane; v < side_1 * F::kRows * n_tok; v += 32) {
+              const int r = v % F::kRows, at = v / F::kRows % side_1, tok = v / (F::kRows * side_1);
+              const int c = (tile * side_1 + at) * F::kRows + r;
+              const float sum = add_up(red + at * step * F::kRows * 4 + red_4(r, tok), F::kRows * 4, step);
+              if (c < p.hidden) p.part[static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.hidden + c] = sum;
             }
           }
+          __syncwarp();
+          if (lane == 0) {
+            tma::mbar_arrive(free_bar + 8 * buf);
+            if (!await_count(&s_told, round - kQueue + 1)) atomicOr(p.err, kErrTimeout);
+            queue[round % kQueue] = static_cast<uint16_t>(phase == 0 ? job.expert : tile);
+            __threadfence_block();
+            *static_cast<volatile int*>(&s_written[buf]) = (round >> 1) + 1;
+          }
         }
-        __syncthreads();   // s_flag may change again
+      }
+    }
+  } else {
+    // ---- the warp that tells: rounds [told, upto) are written, one fence for all of them
+    const int rounds_1 = s_rounds;
+    int total[2] = {0, 0};
+    for (int ph = 0; ph < 2; ++ph) {
+      int job_i = 0, tile = first(ph);
+      for (;; tile += grid) {
+        while (tile >= tiles(ph)) tile -= tiles(ph), ++job_i;
+        if (job_i >= jobs_of(ph)) break;
+        total[ph] += pick(ph, (job_at(ph, job_i).count + 7) >> 3, (job_at(ph, job_i).count + 3) >> 2);
+      }
+    }
+    const int rounds = total[0] + total[1];
+    for (int told = 0; told < rounds;) {
+      if (!await_count(&s_written[told & 1], (told >> 1) + 1) && lane == 0) atomicOr(p.err, kErrTimeout);
+      __syncwarp();
+      const int w0 = *static_cast<volatile int*>(&s_written[0]), w1 = *static_cast<volatile int*>(&s_written[1]);
+      // even rounds below 2 w0 and odd rounds below 2 w1 are written
+      const int upto = max(told + 1, min(min(2 * w0, 2 * w1 + 1), told + 32));
+      __threadfence();
+      __syncwarp();
+      const int r = __shfl_sync(kAll, told, 0) + lane;
+      if (r < __shfl_sync(kAll, upto, 0)) {
+        const int what = *static_cast<volatile uint16_t*>(&queue[r % kQueue]);
+        if (r < total[0])
+          atomicAdd(p.ready + what, 1);
+        else if (atomicAdd(p.tile_done + what, 1) == rounds_1 - 1)
+          finished[atomicAdd(&s_finished, 1)] = static_cast<uint16_t>(what);
+      }
+      told = __shfl_sync(kAll, upto, 0);
+      if (lane == 0) *static_cast<volatile int*>(&s_told) = told;
+    }
+  }
+  __threadfence();
+  __syncthreads();         // `finished` is complete
+  {
+    const int n_done = s_finished, rows = side_1 * F::kRows;
+    for (int f = 0; f < n_done; ++f) {
+      for (int v = tid; v < rows * p.n; v += kThreads) {
+        const int tok = v / rows, c = finished[f] * rows + v % rows;
+        if (c >= p.hidden) continue;
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < p.topk; ++k) {
+          const int en = tok * p.topk + k;
+          const float y = __ldcg(p.part + static_cast<int64_t>(en) * p.hidden + c);
+          if (L.valid[en / 32] >> (en % 32) & 1) sum = fmaf(p.topk_weights[en], y, sum);
+        }
+        const int64_t o = static_cast<int64_t>(tok) * p.hidden + c;
+        if (p.bias) sum += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[o]);
+        if (p.out_f32)
+          static_cast<float*>(p.out)[o] = sum;
+        else
+          static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum);
       }
     }
   }
@@ -481,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
   }
   __syncthreads();
   if (s_flag) {
-    for (int i = tid; i < actives; i += kThreads) p.ready[i] = 0;
+    for (int i = tid; i < p.experts; i += kThreads) p.ready[i] = 0;
     for (int i = tid; i < tiles_1; i += kThreads) p.tile_done[i] = 0;
     if (tid == 0) *p.blocks_done = 0;
   }
@@ -490,13 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeParams p) {
 template <int G, int NT>
 cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   using S = Shape<G, NT>;
-  const int bytes = S::kRing + S::kRed + lists_bytes(p.n * p.topk);
+  const int bytes = S::kRing + 2 * S::kRed + lists_bytes(p.n * p.topk);
   if (const cudaError_t e = cudaFuncSetAttribute(moe_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
       e != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -510,9 +698,6 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
 template <int G>
 cudaError_t launch_g(const MoeParams& p, int num_sms, cudaStream_t s) {
   if (p.n <= 8) return launch<G, 1>(p, num_sms, s);
-  if constexpr (G == 0) {
-    if (p.n > 16) return launch<G, 4>(p, num_sms, s);
-  }
   return launch<G, 2>(p, num_sms, s);
 }
 

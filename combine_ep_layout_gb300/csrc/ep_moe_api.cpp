@@ -283,7 +283,7 @@ int ep_moe_create(const ep_moe_cfg_t* cfg, ep_moe_t* out) noexcept {
     const size_t n_h = up(entries * cfg->intermediate_dim * 4);
     const size_t n_part = up(entries * cfg->hidden_dim * sizeof(float));
     const size_t n_tile = static_cast<size_t>(cfg->hidden_dim + 15) / 16;
-    const size_t total = n_h + n_part + up(sizeof(int32_t) * (entries + n_tile + 2));
+    const size_t total = n_h + n_part + up(sizeof(int32_t) * (cfg->num_experts + n_tile + 2));
     if ((e = cudaStreamCreateWithFlags(&m->own_stream, cudaStreamNonBlocking)) != cudaSuccess)
       return bail(fail_cuda(e, "cudaStreamCreateWithFlags"));
     if ((e = cudaMallocAsync(&m->block, total, m->own_stream)) != cudaSuccess) {
@@ -296,7 +296,7 @@ int ep_moe_create(const ep_moe_cfg_t* cfg, ep_moe_t* out) noexcept {
     m->h = b;
     m->part = reinterpret_cast<float*>(b + n_h);
     m->ready = reinterpret_cast<int32_t*>(b + n_h + n_part);
-    m->tile_done = m->ready + entries;
+    m->tile_done = m->ready + cfg->num_experts;
     m->blocks_done = m->tile_done + n_tile;
     m->err = m->blocks_done + 1;
     if ((e = cudaMemsetAsync(m->block, 0, total, m->own_stream)) != cudaSuccess)

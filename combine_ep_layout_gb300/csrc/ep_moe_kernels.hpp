@@ -59,8 +59,8 @@ struct MoeParams {
   void* h;                  // bf16 [max_tokens * K, 2, I]: the upper and the lower half of h
   float* part;              // [max_tokens * K, H]
   // counters, zero between launches
-  int32_t* ready;           // [min(E, max_tokens * K)] finished gate/up items by active expert
-  int32_t* tile_done;       // [H / 16] finished down items by channel tile
+  int32_t* ready;           // [E] finished gate/up rounds by expert
+  int32_t* tile_done;       // [H / 16] finished down rounds by channel tile
   int32_t* blocks_done;     // [1]
   int32_t* err;
   uint64_t wait_ns;

@@ -180,37 +180,28 @@ __device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT
   }
 }
 
-// Copy the scales of stage c: kScales of each of the tile's rows.  `row_of(r)`
-// gives the matrix row of tile row r; `wide` when every row's scales of a stage
-// are whole and aligned.
+// Copy the scales of stage c one by one: kScales of each of the tile's rows,
+// zeros past the end of a row.  `row_of(r)` gives the matrix row of tile row r.
 template <int G, int RT, class RowOf>
-__device__ __forceinline__ void copy_scales(uint32_t slot, int lane, const float* scales, int cols, int c, bool wide,
+__device__ __forceinline__ void copy_scales(uint32_t slot, int lane, const float* scales, int cols, int c,
                                             RowOf row_of) {
   using F = Form<G, RT>;
-  if constexpr (F::kInt4) {
-    const int groups = cols / G;
-    if (wide) {
-#pragma unroll
-      for (int i = 0; i < (F::kRows + 31) / 32; ++i) {
-        const int r = lane + 32 * i;
-        if (F::kRows < 32 && r >= F::kRows) break;
-        const float* src = scales + static_cast<int64_t>(row_of(r)) * groups + c * F::kScales;
-        const uint32_t dst = slot + F::kABytes + 4 * F::kScales * r;
-        if constexpr (F::kScales == 4)
-          copy16(dst, src, true);
-        else
-          copy_small<4 * F::kScales>(dst, src, true);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < (F::kRows * F::kScales + 31) / 32; ++i) {
-        if (F::kRows * F::kScales < 32 && lane >= F::kRows * F::kScales) break;
-        const int p = lane + 32 * i, r = p / F::kScales, s = c * F::kScales + p % F::kScales;
-        const float* src = scales + static_cast<int64_t>(row_of(r)) * groups;
-        copy_small<4>(slot + F::kABytes + 4 * p, src + (s < groups ? s : 0), s < groups);
-      }
-    }
+  const int groups = cols / G;
+#pragma unroll 1
+  for (int p = lane; p < F::kRows * F::kScales; p += 32) {
+    const int r = p / F::kScales, s = c * F::kScales + p % F::kScales;
+    const float* src = scales + static_cast<int64_t>(row_of(r)) * groups;
+    copy_small<4>(slot + F::kABytes + 4 * p, src + (s < groups ? s : 0), s < groups);
   }
+}
+
+// One row's scales of a stage at once (aligned to BYTES).
+template <int BYTES>
+__device__ __forceinline__ void copy_wide(uint32_t dst, const float* src) {
+  if constexpr (BYTES == 16)
+    copy16(dst, src, true);
+  else
+    copy_small<BYTES>(dst, src, true);
 }
 
 }  // namespace stream

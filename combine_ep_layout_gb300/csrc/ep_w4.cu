@@ -49,24 +49,43 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
   const bool wide = p.cols % 128 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
   const uint32_t ring = stream::smem_addr(smem) + warp * kStages * S::kSlot;
   auto row_of = [&](int r) { return min(tile * F::kRows + r, p.rows - 1); };
+  const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
   const uint8_t* row_ptr[F::kCopies];
 #pragma unroll
   for (int i = 0; i < F::kCopies; ++i)
-    row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane / F::kPieces + i * (32 / F::kPieces))) * (p.cols / 2);
-  const uint32_t a_dst = F::a_offset(lane / F::kPieces, lane % F::kPieces);
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(t0) * p.cols;
+    row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane_row + i * (32 / F::kPieces))) * (p.cols / 2);
+  const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
+  constexpr int kScaleCopies = (F::kRows + 31) / 32, kXCopies = 8 * NT * F::kXPieces / 32;
+  const float* s_src[kScaleCopies];
+#pragma unroll
+  for (int i = 0; i < kScaleCopies; ++i)
+    s_src[i] = p.scales + static_cast<int64_t>(row_of(lane + 32 * i)) * (p.cols / G);
+  const int lane_col = lane / F::kXPieces, lane_xpiece = lane % F::kXPieces;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(t0 + lane_col) * p.cols;
   auto issue = [&](int c, uint32_t slot) {
     if (c < chunks) {
-      const int piece = c * F::kPieces + lane % F::kPieces;
+      const int piece = c * F::kPieces + lane_piece;
       const bool ok = piece < pieces;
+      const int w_at = ok ? piece * 16 : 0;
 #pragma unroll
       for (int i = 0; i < F::kCopies; ++i)
-        stream::copy16(slot + a_dst + i * (32 / F::kPieces) * F::kRowBytes, row_ptr[i] + (ok ? piece * 16 : 0), ok);
-      stream::copy_scales<G, RT>(slot, lane, p.scales, p.cols, c, wide, row_of);
-      for (int q = lane; q < cols * F::kXPieces; q += 32) {
-        const int col = q / F::kXPieces, k = c * F::kCols + 8 * (q % F::kXPieces);
-        stream::copy16(slot + F::x_offset(col, q % F::kXPieces),
-                       x + static_cast<int64_t>(col) * p.cols + (k < p.cols ? k : 0), k < p.cols);
+        stream::copy16(slot + a_dst + i * (32 / F::kPieces) * F::kRowBytes, row_ptr[i] + w_at, ok);
+      if (wide) {
+#pragma unroll
+        for (int i = 0; i < kScaleCopies; ++i)
+          if (F::kRows >= 32 || lane < F::kRows)
+            stream::copy_wide<4 * F::kScales>(slot + F::kABytes + 4 * F::kScales * (lane + 32 * i), s_src[i] + c * F::kScales);
+      } else {
+        stream::copy_scales<G, RT>(slot, lane, p.scales, p.cols, c, row_of);
+      }
+      const int at = c * F::kCols + 8 * lane_xpiece;
+      const int x_at = at < p.cols ? at : 0;
+#pragma unroll
+      for (int i = 0; i < kXCopies; ++i) {
+        const int col = lane_col + i * (32 / F::kXPieces);
+        if (col < cols)
+          stream::copy16(slot + F::x_offset(col, lane_xpiece),
+                         x + static_cast<int64_t>(i * (32 / F::kXPieces)) * p.cols + x_at, at < p.cols);
       }
     }
     stream::commit();
@@ -100,6 +119,16 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
       *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
       *reinterpret_cast<float2*>(r0 + 8 * S::kRedRow) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
     }
+  __syncthreads();
+  // each thread adds the 8 warps' sums of its values and keeps them in the first
+  // warp's place, which nothing else reads
+  for (int v = tid; v < F::kRows * cols; v += kThreads) {
+    float* at = red + (v / cols) * S::kRedRow + v % cols;
+    float sum = *at;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum += at[w * F::kRows * S::kRedRow];
+    *at = sum;
+  }
   cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
   if (splits > 1)
     cl.sync();
@@ -110,11 +139,10 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
     const int r = v % F::kRows, col = v / F::kRows;
     const int row = tile * F::kRows + r;
     if (row >= p.rows) continue;
-    float sum = 0.0f;
-    for (int b = 0; b < splits; ++b) {
-      const float* from = splits > 1 ? cl.map_shared_rank(red, b) : red;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += from[(w * F::kRows + r) * S::kRedRow + col];
+    float sum = red[r * S::kRedRow + col];
+    if (splits > 1) {
+      sum = 0.0f;
+      for (int b = 0; b < splits; ++b) sum += cl.map_shared_rank(red, b)[r * S::kRedRow + col];
     }
     const int64_t o = static_cast<int64_t>(t0 + col) * p.rows + row;
     if (p.out_f32)
