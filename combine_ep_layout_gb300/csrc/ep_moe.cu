@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ep_moe_kernels.hpp"
@@ -135,9 +136,11 @@ struct Shape {
   // 4 row tiles spare 4-bit weights half the work on the activations; with 16
   // columns they would leave the ring too short
   static constexpr int kRowTiles = G != 0 && NT == 1 ? 4 : 2;
-  static constexpr int kEnough = 8;                          // stages of a warp in an item (see widen)
+  // tokens of one job: gate/up a column each, down two columns each
+  static constexpr int kCap0 = 8 * NT, kCap1 = 4 * NT;
+  static constexpr int kEnough = 8, kItems = 4;              // stages of a warp in an item, items of a block (see widen)
   using F = Form<G, kRowTiles>;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = G != 0 && NT == 1 ? 12 : 8;
   static constexpr int kAllWarps = kWarps + kFinishers + 1;
   static constexpr int kThreads = 32 * kAllWarps;
   static constexpr int kTokens = NT == 1 ? 8 : kFewTokens;   // most tokens of a call
@@ -146,7 +149,7 @@ struct Shape {
   static constexpr int kFit = (kSmemLimit - 2 * kRed - lists_bytes(kTokens * 16)) / (kWarps * kSlot);
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kRing = kWarps * kStages * kSlot;
-  static_assert(kStages >= 3 && 8 * NT <= 16);
+  static_assert(kStages >= 2);
   // the expert counts of the set-up (2048 x 4 bytes) and the ranks use the ring
   static_assert(kRing >= 4 * 2048 + 4 * kMaxEntries);
 };
@@ -216,8 +219,8 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     const int e1 = min(e0 + per, p.experts);
     auto word = [](int c) -> uint64_t {
       return c == 0 ? 0
-                    : static_cast<uint64_t>(c) | static_cast<uint64_t>((c + 8 * NT - 1) / (8 * NT)) << 16 |
-                          static_cast<uint64_t>((c + 4 * NT - 1) / (4 * NT)) << 32;
+                    : static_cast<uint64_t>(c) | static_cast<uint64_t>((c + S::kCap0 - 1) / S::kCap0) << 16 |
+                          static_cast<uint64_t>((c + S::kCap1 - 1) / S::kCap1) << 32;
     };
     uint64_t mine = 0;
     int rounds = 0;        // down rounds of one channel tile
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       if (c == 0) continue;
       const int start = static_cast<int>(base & 0xffff);
       for (int ph = 0; ph < 2; ++ph) {
-        const int cap = ph == 0 ? 8 * NT : 4 * NT;
+        const int cap = ph == 0 ? S::kCap0 : S::kCap1;
         int j = static_cast<int>(base >> (16 + 16 * ph) & 0xffff);
         for (int o = 0; o < c; o += cap, ++j)
           (ph == 0 ? L.jobs_0 : L.jobs_1)[j] = pack_job(e, start + o, min(cap, c - o), (c + 7) >> 3);
@@ -273,15 +276,14 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   // warps: where the columns are few, one tile would give a warp so few stages that
   // setting them up costs more than they do.  As long as every block keeps enough
   // items for all to end together.
-  auto widen = [&](int subtiles, int jobs, int n_chunks) {
-    int r = 1;
-    while (r < 4 && n_chunks * r < S::kEnough * kWarps && jobs * ((subtiles + 2 * r - 1) / (2 * r)) >= 12 * grid) r *= 2;
+  auto widen = [&](int subtiles, int jobs, int n_chunks) {   // the logarithm of the tiles
+    int r = 0;
+    while (r < 2 && (n_chunks << r) < S::kEnough * kWarps && jobs * (((subtiles - 1) >> (r + 1)) + 1) >= S::kItems * grid) ++r;
     return r;
   };
   const int sub_0 = (p.inter + kHalf - 1) / kHalf, sub_1 = (p.hidden + F::kRows - 1) / F::kRows;
   const int side_0 = widen(sub_0, jobs_0, chunks_0), side_1 = widen(sub_1, jobs_1, chunks_1);
-  auto side = [&](int ph) { return pick(ph, side_0, side_1); };
-  const int tiles_0 = (sub_0 + side_0 - 1) / side_0, tiles_1 = (sub_1 + side_1 - 1) / side_1;
+  const int tiles_0 = ((sub_0 - 1) >> side_0) + 1, tiles_1 = ((sub_1 - 1) >> side_1) + 1;
   auto tiles = [&](int ph) { return pick(ph, tiles_0, tiles_1); };
   auto jobs_of = [&](int ph) { return pick(ph, jobs_0, jobs_1); };
   auto job_at = [&](int ph, int j) { return unpack_job(pick(ph, L.jobs_0, L.jobs_1)[j]); };
@@ -298,9 +300,11 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   // This warp's place in an item: row tile `sub` of it, and chunk c = lead, lead +
   // step, ... of the columns; an item's last chunk is followed by the next item's
   // first, so that no warp has more chunks than another in the long run.
-  auto step = [&](int ph) { return kWarps / side(ph); };
-  auto sub = [&](int ph) { return warp / step(ph); };
-  auto lead = [&](int ph) { return warp % step(ph); };
+  const int step_0 = kWarps >> side_0, step_1 = kWarps >> side_1;
+  const int at_0 = warp / step_0, at_1 = warp / step_1, lead_0 = warp % step_0, lead_1 = warp % step_1;
+  auto step = [&](int ph) { return pick(ph, step_0, step_1); };
+  auto lead = [&](int ph) { return pick(ph, lead_0, lead_1); };
+  auto sub_tile = [&](int ph, int tile) { return pick(ph, (tile << side_0) + at_0, (tile << side_1) + at_1); };
   struct Walk {
     int ph, job, tile, c;
   };
@@ -334,11 +338,12 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
   const int lane_col = lane / F::kXPieces, lane_xpiece = lane % F::kXPieces;
   const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
-  const uint8_t* w_src = nullptr;           // the expert's matrix, at this lane's piece
-  uint32_t row_off[F::kCopies];             // 16-byte units
+  const uint8_t *w_lo = nullptr, *w_hi = nullptr;   // this lane's first row of either half of the tile
+  uint32_t w_step = 0;                      // bytes from one of its rows to the next
+  int w_left = 0;                           // rows of a half that exist (gate/up: of either; down: of the tile)
   const float* s_src[F::kRows / 32] = {};   // of tile rows `lane`, `lane` + 32
   auto channel_row = [&](int ph, int tile, int r) {
-    const int at = tile * side(ph) + sub(ph);
+    const int at = sub_tile(ph, tile);
     if (ph == 1) return min(at * F::kRows + r, p.hidden - 1);
     const int ch = min(at * kHalf + (r < kHalf ? r : r - kHalf), p.inter - 1);
     return r < kHalf ? ch : p.inter + ch;
@@ -348,25 +353,43 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
            static_cast<int64_t>(job_at(w.ph, w.job).expert) * pick(w.ph, 2 * p.inter, p.hidden) * (dim_k(w.ph) / (F::kInt4 ? G : 1));
   };
   auto enter_weights = [&](const Walk& w) {
-    const uint32_t pieces = dim_k(w.ph) / F::kPerPiece;
-    const int64_t rows = pick(w.ph, 2 * p.inter, p.hidden);
-    w_src = static_cast<const uint8_t*>(pick(w.ph, p.w13, p.w2)) +
-            (job_at(w.ph, w.job).expert * rows * pieces + lane_piece) * 16;
-#pragma unroll
-    for (int i = 0; i < F::kCopies; ++i)
-      row_off[i] = static_cast<uint32_t>(channel_row(w.ph, w.tile, lane_row + i * (32 / F::kPieces))) * pieces;
+    // rows of a tile that do not exist (the last tile's) are zeros
+    const int64_t row_bytes = dim_k(w.ph) / F::kPerPiece * 16;
+    const int at = sub_tile(w.ph, w.tile), row = at * pick(w.ph, kHalf, F::kRows);
+    w_left = pick(w.ph, p.inter, p.hidden) - row;
+    w_lo = static_cast<const uint8_t*>(pick(w.ph, p.w13, p.w2)) + lane_piece * 16 +
+           (static_cast<int64_t>(job_at(w.ph, w.job).expert) * pick(w.ph, 2 * p.inter, p.hidden) + row + lane_row) * row_bytes;
+    w_hi = w_lo + pick(w.ph, p.inter, kHalf) * row_bytes;
+    w_step = static_cast<uint32_t>(row_bytes) * (32 / F::kPieces);
     if constexpr (F::kInt4) {
+      const float* scales = expert_scales(w);
 #pragma unroll
       for (int i = 0; i < F::kRows / 32; ++i)
-        s_src[i] = expert_scales(w) + static_cast<int64_t>(channel_row(w.ph, w.tile, lane + 32 * i)) * (dim_k(w.ph) / G);
+        s_src[i] = scales + static_cast<int64_t>(channel_row(w.ph, w.tile, lane + 32 * i)) * (dim_k(w.ph) / G);
     }
   };
   auto copy_weights = [&](const Walk& w, uint32_t slot) {
     const bool ok = w.c * F::kPieces + lane_piece < dim_k(w.ph) / F::kPerPiece;
-    const uint8_t* src = w_src + (ok ? w.c * F::kRowBytes : 0);
+    const int64_t at = ok ? w.c * F::kRowBytes : 0;
+    const uint8_t *lo = w_lo + at, *hi = w_hi + at;
+    const uint32_t dst = slot + a_dst;
+    constexpr int kEach = F::kCopies / 2, kPitch = 32 / F::kPieces * F::kRowBytes;
+    if (w_left >= pick(w.ph, kHalf, F::kRows)) {
 #pragma unroll
-    for (int i = 0; i < F::kCopies; ++i)
-      stream::copy16(slot + a_dst + i * (32 / F::kPieces) * F::kRowBytes, src + static_cast<uint64_t>(row_off[i]) * 16, ok);
+      for (int i = 0; i < kEach; ++i) stream::copy16(dst + i * kPitch, lo + static_cast<uint64_t>(i) * w_step, ok);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) stream::copy16(dst + (kEach + i) * kPitch, hi + static_cast<uint64_t>(i) * w_step, ok);
+    } else {
+      const int left_hi = pick(w.ph, w_left, w_left - kHalf);
+      const uint8_t* none = static_cast<const uint8_t*>(pick(w.ph, p.w13, p.w2));   // read by nobody
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = lane_row + i * (32 / F::kPieces);
+        const bool ok_lo = ok && r < w_left, ok_hi = ok && r < left_hi;
+        stream::copy16(dst + i * kPitch, ok_lo ? lo + static_cast<uint64_t>(i) * w_step : none, ok_lo);
+        stream::copy16(dst + (kEach + i) * kPitch, ok_hi ? hi + static_cast<uint64_t>(i) * w_step : none, ok_hi);
+      }
+    }
     if constexpr (F::kInt4) {
       if (pick(w.ph, whole_0, whole_1)) {
 #pragma unroll
@@ -542,7 +565,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       return sum;
     };
     for (int phase = 0; phase < 2; ++phase) {
-      const int step = kWarps / side(phase);
+      const int step = kWarps >> pick(phase, side_0, side_1);
       int job_i = 0, tile = first(phase);
       for (;; tile += grid) {
         while (tile >= tiles(phase)) tile -= tiles(phase), ++job_i;
@@ -554,9 +577,9 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
           bar_sync<32 * (kWarps + 1)>(kBarFull + buf);
           if (phase == 0) {
             const int n_cols = min(8, cols - 8 * nt);
-            for (int v = lane; v < side_0 * kHalf * n_cols; v += 32) {
-              const int ch = v % kHalf, at = v / kHalf % side_0, col = v / (kHalf * side_0);
-              const int i = (tile * side_0 + at) * kHalf + ch;
+            for (int v = lane; v < kHalf * n_cols << side_0; v += 32) {
+              const int ch = v % kHalf, at = v / kHalf & ((1 << side_0) - 1), col = v / kHalf >> side_0;
+              const int i = ((tile << side_0) + at) * kHalf + ch;
               const float* from = red + at * step * F::kRows * 8;
               const float gate = add_up(from + red_8(ch, col), F::kRows * 8, step);
               const float up = add_up(from + red_8(kHalf + ch, col), F::kRows * 8, step);
@@ -574,9 +597,9 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
             }
           } else {
             const int n_tok = min(4, job.count - 4 * nt);
-            for (int v = lane; v < side_1 * F::kRows * n_tok; v += 32) {
-              const int r = v % F::kRows, at = v / F::kRows % side_1, tok = v / (F::kRows * side_1);
-              const int c = (tile * side_1 + at) * F::kRows + r;
+            for (int v = lane; v < F::kRows * n_tok << side_1; v += 32) {
+              const int r = v % F::kRows, at = v / F::kRows & ((1 << side_1) - 1), tok = v / F::kRows >> side_1;
+              const int c = ((tile << side_1) + at) * F::kRows + r;
               const float sum = add_up(red + at * step * F::kRows * 4 + red_4(r, tok), F::kRows * 4, step);
               if (c < p.hidden) p.part[static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.hidden + c] = sum;
             }
@@ -628,10 +651,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   __threadfence();
   __syncthreads();         // `finished` is complete
   {
-    const int n_done = s_finished, rows = side_1 * F::kRows;
+    const int n_done = s_finished, rows = F::kRows << side_1;
     for (int f = 0; f < n_done; ++f) {
       for (int v = tid; v < rows * p.n; v += kThreads) {
-        const int tok = v / rows, c = finished[f] * rows + v % rows;
+        const int tok = v / F::kRows >> side_1, c = finished[f] * rows + (v & (rows - 1));
         if (c >= p.hidden) continue;
         float sum = 0.0f;
 #pragma unroll 8
@@ -678,10 +701,17 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
 template <int G, int NT>
 cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   using S = Shape<G, NT>;
+  static std::atomic<uint64_t> ready{0};   // devices on which the shared-memory limit is raised
   const int bytes = S::kRing + 2 * S::kRed + lists_bytes(p.n * p.topk);
-  if (const cudaError_t e = cudaFuncSetAttribute(moe_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-      e != cudaSuccess)
-    return e;
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    if (const cudaError_t e = cudaFuncSetAttribute(moe_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        e != cudaSuccess)
+      return e;
+    if (dev < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
   cfg.blockDim = dim3(S::kThreads);

@@ -65,6 +65,15 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = a b
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Two of a word's nibbles (bits 0-3 and 16-19 of v) as bf16 values nibble - 8:
 // with 0x43 above it a nibble reads as the bf16 128 + nibble, exactly.
 __device__ __forceinline__ uint32_t nibble_pair(uint32_t v) {
@@ -99,14 +108,18 @@ struct Form {
   __device__ static __forceinline__ uint32_t a_offset(int r, int c) {
     return static_cast<uint32_t>(r * kRowBytes + 16 * (kInt4 ? c ^ ((r >> 1) & 3) : c ^ ((r & 1) << 2)));
   }
-  __device__ static __forceinline__ uint32_t x_offset(int col, int c) {
-    return static_cast<uint32_t>(kABytes + kSBytes + col * kXBytes + 16 * (c ^ ((col & 1) << 2)));
+  // Where piece c of activation column col lies, from the columns' start and from
+  // the stage's (weights, scales, columns).
+  __device__ static __forceinline__ uint32_t x_at(int col, int c) {
+    return static_cast<uint32_t>(col * kXBytes + 16 * (c ^ ((col & 1) << 2)));
   }
+  __device__ static __forceinline__ uint32_t x_offset(int col, int c) { return kABytes + kSBytes + x_at(col, c); }
 };
 
-// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of the stage at `slot`.
+// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
+// and scales at `slot`, columns at `cols`.
 template <int G, int RT, int NT, int CAP>
-__device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT][CAP][4]) {
+__device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lane, float (&acc)[RT][CAP][4]) {
   using F = Form<G, RT>;
   const int g = lane >> 2, t = lane & 3;
   if constexpr (!F::kInt4) {
@@ -120,7 +133,7 @@ __device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint4 x = lds128(slot + F::x_offset(8 * nt + g, 4 * kk + t));
+        const uint4 x = lds128(cols + F::x_at(8 * nt + g, 4 * kk + t));
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
           mma(acc[rt][nt], lo[rt].x, hi[rt].x, lo[rt].y, hi[rt].y, x.x, x.y);
@@ -135,17 +148,11 @@ __device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT
     for (int grp = 0; grp < F::kScales; ++grp) {
       float sum[F::kRowTiles][NT][4];
 #pragma unroll
-      for (int rt = 0; rt < F::kRowTiles; ++rt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[rt][nt][i] = 0.0f;
-#pragma unroll
       for (int q = grp * (G / 32); q < (grp + 1) * (G / 32); ++q) {
         uint32_t b[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 x = lds128(slot + F::x_offset(8 * nt + g, 4 * q + t));
+          const uint4 x = lds128(cols + F::x_at(8 * nt + g, 4 * q + t));
           b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
           b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
           b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
@@ -159,7 +166,10 @@ __device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT
                                  nibble_pair(lo >> 8), nibble_pair(hi >> 8), nibble_pair(lo >> 12), nibble_pair(hi >> 12)};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+            if (q == grp * (G / 32))
+              mma_first(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+            else
+              mma(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
             mma(sum[rt][nt], a[4], a[5], a[6], a[7], b[nt][2], b[nt][3]);
           }
         }
@@ -178,6 +188,11 @@ __device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT
       }
     }
   }
+}
+
+template <int G, int RT, int NT, int CAP>
+__device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT][CAP][4]) {
+  consume_at<G, RT, NT, CAP>(slot, slot + Form<G, RT>::x_offset(0, 0), lane, acc);
 }
 
 // Copy the scales of stage c one by one: kScales of each of the tile's rows,

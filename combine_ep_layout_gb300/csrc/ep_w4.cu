@@ -1,9 +1,17 @@
 // ep_w4.cu -- products of a few activation rows with a 4-bit weight matrix
 // (include/ep_gb300_moe.h: the form of the weights and the formula).
 //
-// Bound by reading the weights once.  A block of 8 warps takes a tile of 16 RT
-// rows; its warps split the columns chunk by chunk, each through its own
-// cp.async ring (ep_stream.cuh), and add their sums through shared memory.
+// Bound by reading the weights once, as long as turning nibbles into operands
+// keeps up.  Two kernels, by the number of tokens:
+//
+//   narrow (up to 8 tokens)  a block of 8 warps takes 16 RT rows; its warps split
+//       the columns chunk by chunk, each through its own cp.async ring
+//       (ep_stream.cuh), and add their sums through shared memory.  Small tiles
+//       and many blocks: a few MB of weights have to reach every SM at once.
+//   wide (9 to 64 tokens)    each of the 8 warps takes its own 16 RT rows and all
+//       share a stage's activations, which would outweigh the weights if every
+//       warp had its own.
+//
 // Where the rows give too few blocks, a cluster of blocks shares a tile: each
 // takes its part of the columns, and the blocks' sums are added in rank order
 // through distributed shared memory.  No order is left to chance.
@@ -11,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ep_moe_kernels.hpp"
@@ -24,30 +33,65 @@ using stream::Form;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-template <int G, int RT, int NT>
-struct Shape {
+__device__ __forceinline__ void store(const W4Params& p, int token, int row, float v) {
+  const int64_t o = static_cast<int64_t>(token) * p.rows + row;
+  if (p.out_f32)
+    static_cast<float*>(p.out)[o] = v;
+  else
+    static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+}
+
+// The sums of a tile (`rows` x `cols`, kRow floats a row) of every block of the
+// cluster, added in rank order and stored: each block finishes its share.
+template <int kRow>
+__device__ __forceinline__ void finish(const W4Params& p, float* red, int rows, int cols, int row0, int part, int splits) {
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+  if (splits > 1)
+    cl.sync();
+  else
+    __syncthreads();
+  for (int v = part * kThreads + threadIdx.x; v < rows * cols; v += splits * kThreads) {
+    const int r = v % rows, col = v / rows;
+    if (row0 + r >= p.rows) continue;
+    float sum = red[r * kRow + col];
+    if (splits > 1) {
+      sum = 0.0f;
+      for (int b = 0; b < splits; ++b) sum += cl.map_shared_rank(red, b)[r * kRow + col];
+    }
+    store(p, col, row0 + r, sum);
+  }
+  if (splits > 1) cl.sync();   // no block leaves while another reads its sums
+}
+
+// ------------------------------------------------------------------ narrow
+
+template <int G, int RT>
+struct Narrow {
   using F = Form<G, RT>;
-  static constexpr int kSlot = F::stage_bytes(NT);
-  static constexpr int kStages = 3;
-  static constexpr int kRing = kWarps * kStages * kSlot;
-  static constexpr int kRedRow = 8 * NT + 2;                     // floats of a row of one warp's sums
-  static constexpr int kRed = kWarps * F::kRows * kRedRow * 4;
-  static constexpr int kBytes = kRing > kRed ? kRing : kRed;     // the sums come after the ring's last use
+  static constexpr int kStages = RT == 1 ? 6 : 4;
+  static constexpr int kRow = 10;                                // floats of a row of one warp's sums
+  static constexpr int kRed = kWarps * F::kRows * kRow * 4;
+  // the columns that no token fills are read (and not used) past the last slot
+  static constexpr int slot(int n) { return F::kABytes + F::kSBytes + n * F::kXBytes; }
+  static constexpr int bytes(int n) {
+    const int ring = kWarps * kStages * slot(n) + (8 - n) * F::kXBytes;
+    return ring > kRed ? ring : kRed;
+  }
 };
 
-template <int G, int RT, int NT>
-__global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int splits) {
+template <int G, int RT>
+__global__ void __launch_bounds__(kThreads) w4_narrow_kernel(const W4Params p, int splits) {
   using F = Form<G, RT>;
-  using S = Shape<G, RT, NT>;
+  using S = Narrow<G, RT>;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x / splits, part = blockIdx.x % splits;   // part: the rank in the cluster
-  const int t0 = blockIdx.y * 8 * NT, cols = min(8 * NT, p.n - t0);
   const int pieces = p.cols / 32, chunks = (p.cols + F::kCols - 1) / F::kCols;
   const int step = kWarps * splits, c0 = part * kWarps + warp;
-  const bool wide = p.cols % 128 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
-  const uint32_t ring = stream::smem_addr(smem) + warp * kStages * S::kSlot;
+  const bool whole = p.cols % 128 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
+  const uint32_t slot_bytes = F::kABytes + F::kSBytes + p.n * F::kXBytes;
+  const uint32_t ring = stream::smem_addr(smem) + warp * kStages * slot_bytes;
   auto row_of = [&](int r) { return min(tile * F::kRows + r, p.rows - 1); };
   const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
   const uint8_t* row_ptr[F::kCopies];
@@ -55,13 +99,13 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
   for (int i = 0; i < F::kCopies; ++i)
     row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane_row + i * (32 / F::kPieces))) * (p.cols / 2);
   const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
-  constexpr int kScaleCopies = (F::kRows + 31) / 32, kXCopies = 8 * NT * F::kXPieces / 32;
+  constexpr int kScaleCopies = (F::kRows + 31) / 32, kXCopies = 8 * F::kXPieces / 32;
   const float* s_src[kScaleCopies];
 #pragma unroll
   for (int i = 0; i < kScaleCopies; ++i)
     s_src[i] = p.scales + static_cast<int64_t>(row_of(lane + 32 * i)) * (p.cols / G);
   const int lane_col = lane / F::kXPieces, lane_xpiece = lane % F::kXPieces;
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(t0 + lane_col) * p.cols;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(lane_col) * p.cols;
   auto issue = [&](int c, uint32_t slot) {
     if (c < chunks) {
       const int piece = c * F::kPieces + lane_piece;
@@ -70,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
 #pragma unroll
       for (int i = 0; i < F::kCopies; ++i)
         stream::copy16(slot + a_dst + i * (32 / F::kPieces) * F::kRowBytes, row_ptr[i] + w_at, ok);
-      if (wide) {
+      if (whole) {
 #pragma unroll
         for (int i = 0; i < kScaleCopies; ++i)
           if (F::kRows >= 32 || lane < F::kRows)
@@ -83,9 +127,113 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
 #pragma unroll
       for (int i = 0; i < kXCopies; ++i) {
         const int col = lane_col + i * (32 / F::kXPieces);
-        if (col < cols)
+        if (col < p.n)
           stream::copy16(slot + F::x_offset(col, lane_xpiece),
                          x + static_cast<int64_t>(i * (32 / F::kXPieces)) * p.cols + x_at, at < p.cols);
+      }
+    }
+    stream::commit();
+  };
+  float acc[RT][1][4];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[rt][0][i] = 0.0f;
+  for (int s = 0; s < kStages - 1; ++s) issue(c0 + s * step, ring + s * slot_bytes);
+  uint32_t in = ring + (kStages - 1) * slot_bytes, out = ring;
+  const uint32_t end = ring + kStages * slot_bytes;
+  for (int c = c0; c < chunks; c += step) {
+    stream::wait<kStages - 2>();
+    __syncwarp();          // every lane's copies of this stage, and every lane done with the slot refilled next
+    issue(c + (kStages - 1) * step, in);
+    in = in + slot_bytes == end ? ring : in + slot_bytes;
+    stream::consume<G, RT, 1, 1>(out, lane, acc);
+    out = out + slot_bytes == end ? ring : out + slot_bytes;
+  }
+  stream::wait<0>();
+  __syncthreads();         // the rings' memory now holds the sums
+  float* red = reinterpret_cast<float*>(smem);
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    float* r0 = red + (warp * F::kRows + 16 * rt + g) * S::kRow + 2 * t;
+    *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][0][0], acc[rt][0][1]);
+    *reinterpret_cast<float2*>(r0 + 8 * S::kRow) = make_float2(acc[rt][0][2], acc[rt][0][3]);
+  }
+  __syncthreads();
+  // each thread adds the 8 warps' sums of its values and keeps them in the first
+  // warp's place, which nothing else reads
+  for (int v = tid; v < F::kRows * p.n; v += kThreads) {
+    float* at = red + (v % F::kRows) * S::kRow + v / F::kRows;
+    float sum = *at;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum += at[w * F::kRows * S::kRow];
+    *at = sum;
+  }
+  finish<S::kRow>(p, red, F::kRows, p.n, tile * F::kRows, part, splits);
+}
+
+// -------------------------------------------------------------------- wide
+
+template <int G, int RT, int NT>
+struct Wide {
+  using F = Form<G, RT>;
+  static constexpr int kWarpBytes = F::kABytes + F::kSBytes;     // a warp's own part of a stage
+  static constexpr int kXAt = kWarps * kWarpBytes;
+  static constexpr int kSlot = kXAt + 8 * NT * F::kXBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kRows = kWarps * F::kRows;
+  static constexpr int kRow = 8 * NT + 2;
+  static constexpr int kRed = kRows * kRow * 4;
+  static constexpr int kBytes = kStages * kSlot > kRed ? kStages * kSlot : kRed;
+};
+
+template <int G, int RT, int NT>
+__global__ void __launch_bounds__(kThreads, 2) w4_wide_kernel(const W4Params p, int splits) {
+  using F = Form<G, RT>;
+  using S = Wide<G, RT, NT>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tile = blockIdx.x / splits, part = blockIdx.x % splits;
+  const int pieces = p.cols / 32, chunks = (p.cols + F::kCols - 1) / F::kCols;
+  const bool whole = p.cols % 128 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
+  const uint32_t base = stream::smem_addr(smem);
+  auto row_of = [&](int r) { return min(tile * S::kRows + warp * F::kRows + r, p.rows - 1); };
+  const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
+  const uint8_t* row_ptr[F::kCopies];
+#pragma unroll
+  for (int i = 0; i < F::kCopies; ++i)
+    row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane_row + i * (32 / F::kPieces))) * (p.cols / 2);
+  const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
+  const float* s_src = p.scales + static_cast<int64_t>(row_of(lane)) * (p.cols / G);
+  static_assert(F::kRows <= 32);
+  constexpr int kXCopies = 8 * NT * F::kXPieces / kThreads;      // of each thread
+  const int x_col = tid / F::kXPieces, x_piece = tid % F::kXPieces;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(x_col) * p.cols;
+  auto issue = [&](int c, uint32_t slot) {
+    if (c < chunks) {
+      const int piece = c * F::kPieces + lane_piece;
+      const bool ok = piece < pieces;
+      const int w_at = ok ? piece * 16 : 0;
+      const uint32_t own = slot + warp * S::kWarpBytes;
+#pragma unroll
+      for (int i = 0; i < F::kCopies; ++i)
+        stream::copy16(own + a_dst + i * (32 / F::kPieces) * F::kRowBytes, row_ptr[i] + w_at, ok);
+      if (whole) {
+        if (F::kRows >= 32 || lane < F::kRows)
+          stream::copy_wide<4 * F::kScales>(own + F::kABytes + 4 * F::kScales * lane, s_src + c * F::kScales);
+      } else {
+        stream::copy_scales<G, RT>(own, lane, p.scales, p.cols, c, row_of);
+      }
+      const int at = c * F::kCols + 8 * x_piece;
+      const int x_at = at < p.cols ? at : 0;
+#pragma unroll
+      for (int i = 0; i < kXCopies; ++i) {
+        const int col = x_col + i * (kThreads / F::kXPieces);
+        if (col < p.n)
+          stream::copy16(slot + S::kXAt + F::x_at(col, x_piece),
+                         x + static_cast<int64_t>(i * (kThreads / F::kXPieces)) * p.cols + x_at, at < p.cols);
       }
     }
     stream::commit();
@@ -97,95 +245,102 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const W4Params p, int spli
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
-  for (int s = 0; s < kStages - 1; ++s) issue(c0 + s * step, ring + s * S::kSlot);
+  for (int s = 0; s < kStages - 1; ++s) issue(part + s * splits, base + s * S::kSlot);
   int in = kStages - 1, out = 0;
-  for (int c = c0; c < chunks; c += step) {
+  for (int c = part; c < chunks; c += splits) {
     stream::wait<kStages - 2>();
-    __syncwarp();          // every lane's copies of this stage, and every lane done with the slot refilled next
-    issue(c + (kStages - 1) * step, ring + in * S::kSlot);
+    __syncthreads();       // every thread's copies of this stage, and every warp done with the slot refilled next
+    issue(c + (kStages - 1) * splits, base + in * S::kSlot);
     in = in + 1 == kStages ? 0 : in + 1;
-    stream::consume<G, RT, NT, NT>(ring + out * S::kSlot, lane, acc);
+    const uint32_t slot = base + out * S::kSlot;
+    stream::consume_at<G, RT, NT, NT>(slot + warp * S::kWarpBytes, slot + S::kXAt, lane, acc);
     out = out + 1 == kStages ? 0 : out + 1;
   }
   stream::wait<0>();
-  __syncthreads();         // the rings' memory now holds the sums
+  __syncthreads();         // the ring's memory now holds the sums
   float* red = reinterpret_cast<float*>(smem);
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float* r0 = red + (warp * F::kRows + 16 * rt + g) * S::kRedRow + 8 * nt + 2 * t;
+      float* r0 = red + (warp * F::kRows + 16 * rt + g) * S::kRow + 8 * nt + 2 * t;
       *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
-      *reinterpret_cast<float2*>(r0 + 8 * S::kRedRow) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
+      *reinterpret_cast<float2*>(r0 + 8 * S::kRow) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
     }
-  __syncthreads();
-  // each thread adds the 8 warps' sums of its values and keeps them in the first
-  // warp's place, which nothing else reads
-  for (int v = tid; v < F::kRows * cols; v += kThreads) {
-    float* at = red + (v / cols) * S::kRedRow + v % cols;
-    float sum = *at;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum += at[w * F::kRows * S::kRedRow];
-    *at = sum;
-  }
-  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
-  if (splits > 1)
-    cl.sync();
-  else
-    __syncthreads();
-  // each block of the cluster finishes its share of the tile's values
-  for (int v = part * kThreads + tid; v < F::kRows * cols; v += splits * kThreads) {
-    const int r = v % F::kRows, col = v / F::kRows;
-    const int row = tile * F::kRows + r;
-    if (row >= p.rows) continue;
-    float sum = red[r * S::kRedRow + col];
-    if (splits > 1) {
-      sum = 0.0f;
-      for (int b = 0; b < splits; ++b) sum += cl.map_shared_rank(red, b)[r * S::kRedRow + col];
-    }
-    const int64_t o = static_cast<int64_t>(t0 + col) * p.rows + row;
-    if (p.out_f32)
-      static_cast<float*>(p.out)[o] = sum;
-    else
-      static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum);
-  }
-  if (splits > 1) cl.sync();   // no block leaves while another reads its sums
+  finish<S::kRow>(p, red, S::kRows, p.n, tile * S::kRows, part, splits);
 }
 
-template <int G, int RT, int NT>
-cudaError_t launch(const W4Params& p, int splits, cudaStream_t s) {
-  using S = Shape<G, RT, NT>;
-  auto kernel = w4_kernel<G, RT, NT>;
-  if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-      e != cudaSuccess)
-    return e;
+// ------------------------------------------------------------------ launch
+
+// How many blocks of a cluster share a tile: the fewest rounds of the GPU's
+// `slots` block places times the stages of a round (6 stages for its beginning
+// and end), at most the 8 blocks that a cluster may always have.
+int choose_splits(int tiles, int stages, int slots) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= 8; s *= 2) {
+    const int64_t cost = static_cast<int64_t>((static_cast<int64_t>(tiles) * s + slots - 1) / slots) * ((stages + s - 1) / s + 6);
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+template <class K>
+cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, int tiles, int splits, int most_bytes,
+                   int bytes, cudaStream_t s) {
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  // the kernel's shared-memory limit is raised once on each device
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most_bytes);
+        e != cudaSuccess)
+      return e;
+    if (dev < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
-  const int tiles = (p.rows + 16 * RT - 1) / (16 * RT);
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>((p.n + 8 * NT - 1) / (8 * NT)));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * static_cast<unsigned>(splits));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p, splits);
+}
+
+template <int G, int RT>
+cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
+  using S = Narrow<G, RT>;
+  static std::atomic<uint64_t> ready{0};
+  const int tiles = (p.rows + 16 * RT - 1) / (16 * RT), chunks = (p.cols + 127) / 128;
+  const int per_sm = 220000 / S::bytes(p.n) < 1 ? 1 : 220000 / S::bytes(p.n);
+  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 152 * per_sm);
+  return launch(w4_narrow_kernel<G, RT>, ready, p, tiles, splits, S::bytes(8), S::bytes(p.n), s);
+}
+
+template <int G, int RT, int NT>
+cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
+  using S = Wide<G, RT, NT>;
+  static std::atomic<uint64_t> ready{0};
+  const int tiles = (p.rows + S::kRows - 1) / S::kRows, chunks = (p.cols + 127) / 128;
+  return launch(w4_wide_kernel<G, RT, NT>, ready, p, tiles, choose_splits(tiles, chunks, 2 * 152), S::kBytes, S::kBytes, s);
 }
 
 template <int G>
 cudaError_t launch_g(const W4Params& p, cudaStream_t s) {
-  const int rt = p.n <= 2 ? 1 : p.n <= 4 ? 2 : 4;
-  const int tiles = (p.rows + 16 * rt - 1) / (16 * rt);
-  const int chunks = (p.cols + 127) / 128;
-  int splits = 1;
-  while (splits < 8 && tiles * splits < 2 * 152 && chunks >= 2 * 8 * splits) splits *= 2;
-  if (rt == 1) return launch<G, 1, 1>(p, splits, s);
-  if (rt == 2) return launch<G, 2, 1>(p, splits, s);
-  if (p.n <= 8) return launch<G, 4, 1>(p, splits, s);
-  return launch<G, 4, 2>(p, splits, s);
+  // narrow: more rows a block with more tokens, so that the activations stay below
+  // half of what is read
+  if (p.n <= 2) return launch_narrow<G, 1>(p, s);
+  if (p.n <= 4) return launch_narrow<G, 2>(p, s);
+  if (p.n <= 8) return launch_narrow<G, 4>(p, s);
+  if (p.n <= 16) return launch_wide<G, 2, 2>(p, s);
+  if (p.n <= 32) return launch_wide<G, 2, 4>(p, s);
+  return launch_wide<G, 1, 8>(p, s);
 }
 
 }  // namespace
