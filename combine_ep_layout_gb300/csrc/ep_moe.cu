@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
         __syncwarp();      // every lane's copies of this stage, and every lane done with the slot refilled next
         issue(in);
         in = in + 1 == kStages ? 0 : in + 1;
-        const uint32_t slot = ring + out * S::kSlot;
+        const uint8_t* slot = smem + (warp * kStages + out) * S::kSlot;
         out = out + 1 == kStages ? 0 : out + 1;
         if (NT == 1 || nts == 1)
           stream::consume<G, RT, 1, NT>(slot, lane, acc);

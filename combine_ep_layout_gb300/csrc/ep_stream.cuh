@@ -44,17 +44,10 @@ __device__ __forceinline__ void wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds32(a)); }
+// Plain loads of shared memory (pointers into it), which the compiler may move
+// ahead of the arithmetic before them but not past the waits above.
+__device__ __forceinline__ uint4 load16(const uint8_t* at) { return *reinterpret_cast<const uint4*>(at); }
+__device__ __forceinline__ uint32_t load4(const uint8_t* at) { return *reinterpret_cast<const uint32_t*>(at); }
 
 // d += a b: a 16x16 bf16 (row major fragments), b 16x8 bf16, fp32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -119,7 +112,7 @@ struct Form {
 // acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
 // and scales at `slot`, columns at `cols`.
 template <int G, int RT, int NT, int CAP>
-__device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lane, float (&acc)[RT][CAP][4]) {
+__device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* cols, int lane, float (&acc)[RT][CAP][4]) {
   using F = Form<G, RT>;
   const int g = lane >> 2, t = lane & 3;
   if constexpr (!F::kInt4) {
@@ -128,12 +121,12 @@ __device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lan
       uint4 lo[F::kRowTiles], hi[F::kRowTiles];
 #pragma unroll
       for (int rt = 0; rt < F::kRowTiles; ++rt) {
-        lo[rt] = lds128(slot + F::a_offset(16 * rt + g, 4 * kk + t));
-        hi[rt] = lds128(slot + F::a_offset(16 * rt + g + 8, 4 * kk + t));
+        lo[rt] = load16(slot + F::a_offset(16 * rt + g, 4 * kk + t));
+        hi[rt] = load16(slot + F::a_offset(16 * rt + g + 8, 4 * kk + t));
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint4 x = lds128(cols + F::x_at(8 * nt + g, 4 * kk + t));
+        const uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * kk + t));
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
           mma(acc[rt][nt], lo[rt].x, hi[rt].x, lo[rt].y, hi[rt].y, x.x, x.y);
@@ -152,7 +145,7 @@ __device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lan
         uint32_t b[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 x = lds128(cols + F::x_at(8 * nt + g, 4 * q + t));
+          const uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
           b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
           b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
           b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
@@ -160,8 +153,8 @@ __device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lan
         }
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
-          const uint32_t lo = lds32(slot + F::a_offset(16 * rt + g, q) + 4 * t);
-          const uint32_t hi = lds32(slot + F::a_offset(16 * rt + g + 8, q) + 4 * t);
+          const uint32_t lo = load4(slot + F::a_offset(16 * rt + g, q) + 4 * t);
+          const uint32_t hi = load4(slot + F::a_offset(16 * rt + g + 8, q) + 4 * t);
           const uint32_t a[8] = {nibble_pair(lo),      nibble_pair(hi),      nibble_pair(lo >> 4),  nibble_pair(hi >> 4),
                                  nibble_pair(lo >> 8), nibble_pair(hi >> 8), nibble_pair(lo >> 12), nibble_pair(hi >> 12)};
 #pragma unroll
@@ -176,8 +169,8 @@ __device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lan
       }
 #pragma unroll
       for (int rt = 0; rt < F::kRowTiles; ++rt) {
-        const float s0 = lds_f32(slot + F::kABytes + 4 * ((16 * rt + g) * F::kScales + grp));
-        const float s1 = lds_f32(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp));
+        const float s0 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g) * F::kScales + grp)));
+        const float s1 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           acc[rt][nt][0] = fmaf(s0, sum[rt][nt][0], acc[rt][nt][0]);
@@ -191,7 +184,7 @@ __device__ __forceinline__ void consume_at(uint32_t slot, uint32_t cols, int lan
 }
 
 template <int G, int RT, int NT, int CAP>
-__device__ __forceinline__ void consume(uint32_t slot, int lane, float (&acc)[RT][CAP][4]) {
+__device__ __forceinline__ void consume(const uint8_t* slot, int lane, float (&acc)[RT][CAP][4]) {
   consume_at<G, RT, NT, CAP>(slot, slot + Form<G, RT>::x_offset(0, 0), lane, acc);
 }
 

@@ -8,9 +8,10 @@
 //       the columns chunk by chunk, each through its own cp.async ring
 //       (ep_stream.cuh), and add their sums through shared memory.  Small tiles
 //       and many blocks: a few MB of weights have to reach every SM at once.
-//   wide (9 to 64 tokens)    each of the 8 warps takes its own 16 RT rows and all
+//   wide (9 to 64 tokens)    each of a block's 4 warps takes its own 16 rows and all
 //       share a stage's activations, which would outweigh the weights if every
-//       warp had its own.
+//       warp had its own.  Bound by the instructions that make operands of
+//       nibbles and by their latency, so the blocks are small and many.
 //
 // Where the rows give too few blocks, a cluster of blocks shares a tile: each
 // takes its part of the columns, and the blocks' sums are added in rank order
@@ -22,8 +23,10 @@
 #include <atomic>
 #include <cstdint>
 
+#include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
 #include "ep_stream.cuh"
+#include "ep_types.cuh"
 
 namespace epg {
 namespace {
@@ -41,26 +44,49 @@ __device__ __forceinline__ void store(const W4Params& p, int token, int row, flo
     static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
 }
 
-// The sums of a tile (`rows` x `cols`, kRow floats a row) of every block of the
-// cluster, added in rank order and stored: each block finishes its share.
-template <int kRow>
-__device__ __forceinline__ void finish(const W4Params& p, float* red, int rows, int cols, int row0, int part, int splits) {
+// A tile's sums in shared memory: [column][row], 4 floats of padding a column, so
+// that writing fragments and reading rows both miss each other's banks, and what
+// another block of the cluster reads comes in whole 16 bytes (read 4 bytes at a
+// time at strides, the remote reads took 30 us of a 70 us product).
+template <int ROWS>
+__device__ __forceinline__ int sum_at(int row, int col) { return col * (ROWS + 4) + row; }
+
+// The sums of every block of the cluster, added in rank order and stored: each
+// block finishes its share, four rows of a column at a time.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void finish(const W4Params& p, float* red, int cols, int row0, int part, int splits) {
   cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
   if (splits > 1)
     cl.sync();
   else
     __syncthreads();
-  for (int v = part * kThreads + threadIdx.x; v < rows * cols; v += splits * kThreads) {
-    const int r = v % rows, col = v / rows;
+  for (int v = part * THREADS + threadIdx.x; v < ROWS / 4 * cols; v += splits * THREADS) {
+    const int r = v % (ROWS / 4) * 4, col = v / (ROWS / 4), at = sum_at<ROWS>(r, col);
     if (row0 + r >= p.rows) continue;
-    float sum = red[r * kRow + col];
-    if (splits > 1) {
-      sum = 0.0f;
-      for (int b = 0; b < splits; ++b) sum += cl.map_shared_rank(red, b)[r * kRow + col];
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b = 0; b < splits; ++b) {
+      const float4 s = *reinterpret_cast<const float4*>((splits > 1 ? cl.map_shared_rank(red, b) : red) + at);
+      sum.x += s.x, sum.y += s.y, sum.z += s.z, sum.w += s.w;
     }
-    store(p, col, row0 + r, sum);
+    const float each[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row0 + r + i < p.rows) store(p, col, row0 + r + i, each[i]);
   }
   if (splits > 1) cl.sync();   // no block leaves while another reads its sums
+}
+
+// A warp's fragments into such a tile.
+template <int ROWS, int RT, int NT>
+__device__ __forceinline__ void put_sums(float* red, int row0, int lane, const float (&acc)[RT][NT][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[sum_at<ROWS>(row0 + 16 * rt + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1))] = acc[rt][nt][i];
 }
 
 // ------------------------------------------------------------------ narrow
@@ -69,8 +95,8 @@ template <int G, int RT>
 struct Narrow {
   using F = Form<G, RT>;
   static constexpr int kStages = RT == 1 ? 6 : 4;
-  static constexpr int kRow = 10;                                // floats of a row of one warp's sums
-  static constexpr int kRed = kWarps * F::kRows * kRow * 4;
+  static constexpr int kWarpRed = 8 * (F::kRows + 4);            // floats of one warp's sums
+  static constexpr int kRed = kWarps * kWarpRed * 4;
   // the columns that no token fills are read (and not used) past the last slot
   static constexpr int slot(int n) { return F::kABytes + F::kSBytes + n * F::kXBytes; }
   static constexpr int bytes(int n) {
@@ -85,6 +111,7 @@ __global__ void __launch_bounds__(kThreads) w4_narrow_kernel(const W4Params p, i
   using S = Narrow<G, RT>;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
+  allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x / splits, part = blockIdx.x % splits;   // part: the rank in the cluster
   const int pieces = p.cols / 32, chunks = (p.cols + F::kCols - 1) / F::kCols;
@@ -139,61 +166,58 @@ __global__ void __launch_bounds__(kThreads) w4_narrow_kernel(const W4Params p, i
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[rt][0][i] = 0.0f;
+  grid_dependency_wait();   // nothing of memory has been touched before this
   for (int s = 0; s < kStages - 1; ++s) issue(c0 + s * step, ring + s * slot_bytes);
-  uint32_t in = ring + (kStages - 1) * slot_bytes, out = ring;
-  const uint32_t end = ring + kStages * slot_bytes;
+  const uint32_t ring_bytes = kStages * slot_bytes;
+  uint32_t in = (kStages - 1) * slot_bytes, out = 0;
   for (int c = c0; c < chunks; c += step) {
     stream::wait<kStages - 2>();
     __syncwarp();          // every lane's copies of this stage, and every lane done with the slot refilled next
-    issue(c + (kStages - 1) * step, in);
-    in = in + slot_bytes == end ? ring : in + slot_bytes;
-    stream::consume<G, RT, 1, 1>(out, lane, acc);
-    out = out + slot_bytes == end ? ring : out + slot_bytes;
+    issue(c + (kStages - 1) * step, ring + in);
+    in = in + slot_bytes == ring_bytes ? 0 : in + slot_bytes;
+    stream::consume<G, RT, 1, 1>(smem + warp * ring_bytes + out, lane, acc);
+    out = out + slot_bytes == ring_bytes ? 0 : out + slot_bytes;
   }
   stream::wait<0>();
   __syncthreads();         // the rings' memory now holds the sums
   float* red = reinterpret_cast<float*>(smem);
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    float* r0 = red + (warp * F::kRows + 16 * rt + g) * S::kRow + 2 * t;
-    *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][0][0], acc[rt][0][1]);
-    *reinterpret_cast<float2*>(r0 + 8 * S::kRow) = make_float2(acc[rt][0][2], acc[rt][0][3]);
-  }
+  put_sums<F::kRows>(red + warp * S::kWarpRed, 0, lane, acc);
   __syncthreads();
   // each thread adds the 8 warps' sums of its values and keeps them in the first
   // warp's place, which nothing else reads
   for (int v = tid; v < F::kRows * p.n; v += kThreads) {
-    float* at = red + (v % F::kRows) * S::kRow + v / F::kRows;
+    float* at = red + sum_at<F::kRows>(v % F::kRows, v / F::kRows);
     float sum = *at;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum += at[w * F::kRows * S::kRow];
+    for (int w = 1; w < kWarps; ++w) sum += at[w * S::kWarpRed];
     *at = sum;
   }
-  finish<S::kRow>(p, red, F::kRows, p.n, tile * F::kRows, part, splits);
+  finish<F::kRows, kThreads>(p, red, p.n, tile * F::kRows, part, splits);
 }
 
 // -------------------------------------------------------------------- wide
 
-template <int G, int RT, int NT>
+template <int G, int NT>
 struct Wide {
-  using F = Form<G, RT>;
+  using F = Form<G, 1>;
+  static constexpr int kWarps = 4, kThreads = 32 * kWarps;
   static constexpr int kWarpBytes = F::kABytes + F::kSBytes;     // a warp's own part of a stage
   static constexpr int kXAt = kWarps * kWarpBytes;
   static constexpr int kSlot = kXAt + 8 * NT * F::kXBytes;
   static constexpr int kStages = 4;
+  static constexpr int kPerSm = NT == 8 ? 2 : 4;                 // blocks that fit together
   static constexpr int kRows = kWarps * F::kRows;
-  static constexpr int kRow = 8 * NT + 2;
-  static constexpr int kRed = kRows * kRow * 4;
+  static constexpr int kRed = 8 * NT * (kRows + 4) * 4;
   static constexpr int kBytes = kStages * kSlot > kRed ? kStages * kSlot : kRed;
 };
 
-template <int G, int RT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) w4_wide_kernel(const W4Params p, int splits) {
-  using F = Form<G, RT>;
-  using S = Wide<G, RT, NT>;
-  constexpr int kStages = S::kStages;
+template <int G, int NT>
+__global__ void __launch_bounds__(Wide<G, NT>::kThreads, Wide<G, NT>::kPerSm) w4_wide_kernel(const W4Params p, int splits) {
+  using S = Wide<G, NT>;
+  using F = typename S::F;
+  constexpr int kStages = S::kStages, kThreads = S::kThreads, RT = 1;
   extern __shared__ __align__(128) uint8_t smem[];
+  allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x / splits, part = blockIdx.x % splits;
   const int pieces = p.cols / 32, chunks = (p.cols + F::kCols - 1) / F::kCols;
@@ -245,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_wide_kernel(const W4Params p, 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
+  grid_dependency_wait();   // nothing of memory has been touched before this
   for (int s = 0; s < kStages - 1; ++s) issue(part + s * splits, base + s * S::kSlot);
   int in = kStages - 1, out = 0;
   for (int c = part; c < chunks; c += splits) {
@@ -252,43 +277,38 @@ __global__ void __launch_bounds__(kThreads, 2) w4_wide_kernel(const W4Params p, 
     __syncthreads();       // every thread's copies of this stage, and every warp done with the slot refilled next
     issue(c + (kStages - 1) * splits, base + in * S::kSlot);
     in = in + 1 == kStages ? 0 : in + 1;
-    const uint32_t slot = base + out * S::kSlot;
+    const uint8_t* slot = smem + out * S::kSlot;
     stream::consume_at<G, RT, NT, NT>(slot + warp * S::kWarpBytes, slot + S::kXAt, lane, acc);
     out = out + 1 == kStages ? 0 : out + 1;
   }
   stream::wait<0>();
   __syncthreads();         // the ring's memory now holds the sums
   float* red = reinterpret_cast<float*>(smem);
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* r0 = red + (warp * F::kRows + 16 * rt + g) * S::kRow + 8 * nt + 2 * t;
-      *reinterpret_cast<float2*>(r0) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
-      *reinterpret_cast<float2*>(r0 + 8 * S::kRow) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
-    }
-  finish<S::kRow>(p, red, S::kRows, p.n, tile * S::kRows, part, splits);
+  put_sums<S::kRows>(red, warp * F::kRows, lane, acc);
+  finish<S::kRows, S::kThreads>(p, red, p.n, tile * S::kRows, part, splits);
 }
 
 // ------------------------------------------------------------------ launch
 
-// How many blocks of a cluster share a tile: the fewest rounds of the GPU's
-// `slots` block places times the stages of a round (6 stages for its beginning
-// and end), at most the 8 blocks that a cluster may always have.
-int choose_splits(int tiles, int stages, int slots) {
+// How many blocks of a cluster share a tile: the cheapest by the time of its stages,
+// one block's alone (`alone`, its latency) or all of an SM's blocks together
+// (`together` each), in units of 10 ns; a cluster's own cost is 1 us.  At most the
+// 8 blocks that a cluster may always have.
+int choose_splits(int tiles, int stages, int alone, int together) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= 8; s *= 2) {
-    const int64_t cost = static_cast<int64_t>((static_cast<int64_t>(tiles) * s + slots - 1) / slots) * ((stages + s - 1) / s + 6);
+    const int64_t each = (stages + s - 1) / s, per_sm = (static_cast<int64_t>(tiles) * s + 151) / 152;
+    int64_t cost = per_sm * each * together > each * alone ? per_sm * each * together : each * alone;
+    if (s > 1) cost += 100;
     if (cost < least) least = cost, best = s;
   }
   return best;
 }
 
 template <class K>
-cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, int tiles, int splits, int most_bytes,
-                   int bytes, cudaStream_t s) {
+cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, int tiles, int splits, int threads,
+                   int most_bytes, int bytes, cudaStream_t s) {
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
   // the kernel's shared-memory limit is raised once on each device
@@ -301,15 +321,22 @@ cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, in
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * static_cast<unsigned>(splits));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
+  static const bool pdl = PdlEnabled();
+  if (pdl) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (splits > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, p, splits);
 }
 
@@ -318,17 +345,17 @@ cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
   using S = Narrow<G, RT>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + 16 * RT - 1) / (16 * RT), chunks = (p.cols + 127) / 128;
-  const int per_sm = 220000 / S::bytes(p.n) < 1 ? 1 : 220000 / S::bytes(p.n);
-  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 152 * per_sm);
-  return launch(w4_narrow_kernel<G, RT>, ready, p, tiles, splits, S::bytes(8), S::bytes(p.n), s);
+  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 60, 20 * RT);
+  return launch(w4_narrow_kernel<G, RT>, ready, p, tiles, splits, kThreads, S::bytes(8), S::bytes(p.n), s);
 }
 
-template <int G, int RT, int NT>
+template <int G, int NT>
 cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
-  using S = Wide<G, RT, NT>;
+  using S = Wide<G, NT>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + S::kRows - 1) / S::kRows, chunks = (p.cols + 127) / 128;
-  return launch(w4_wide_kernel<G, RT, NT>, ready, p, tiles, choose_splits(tiles, chunks, 2 * 152), S::kBytes, S::kBytes, s);
+  return launch(w4_wide_kernel<G, NT>, ready, p, tiles, choose_splits(tiles, chunks, 90, 12 + 4 * NT), S::kThreads, S::kBytes,
+                S::kBytes, s);
 }
 
 template <int G>
@@ -338,9 +365,9 @@ cudaError_t launch_g(const W4Params& p, cudaStream_t s) {
   if (p.n <= 2) return launch_narrow<G, 1>(p, s);
   if (p.n <= 4) return launch_narrow<G, 2>(p, s);
   if (p.n <= 8) return launch_narrow<G, 4>(p, s);
-  if (p.n <= 16) return launch_wide<G, 2, 2>(p, s);
-  if (p.n <= 32) return launch_wide<G, 2, 4>(p, s);
-  return launch_wide<G, 1, 8>(p, s);
+  if (p.n <= 16) return launch_wide<G, 2>(p, s);
+  if (p.n <= 32) return launch_wide<G, 4>(p, s);
+  return launch_wide<G, 8>(p, s);
 }
 
 }  // namespace
