@@ -34,6 +34,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
 #include "ep_stream.cuh"
 #include "ep_tma.cuh"
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
   __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
   __shared__ uint16_t finished[kMaxTiles];   // the tiles this block folds
+  allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int entries = p.n * p.topk;
   float* red_all = reinterpret_cast<float*>(smem + S::kRing);
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   const uint32_t free_bar = stream::smem_addr(s_free);
   for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
   __syncthreads();
+  grid_dependency_wait();   // no memory of the device has been touched before this
   if (warp == 0) {   // one warp in entry order: the order within an expert is the same in every block
     for (int i0 = 0; i0 < entries; i0 += 32) {
       const int i = i0 + lane;
@@ -717,11 +720,14 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;   // every block resident: the waits on other blocks end
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  static const bool pdl = PdlEnabled();
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT>, p);
 }
 

@@ -1,18 +1,24 @@
 // ep_route.cu -- the router: scores to top-k expert ids and weights, and the
 // gradient of the scores (include/ep_gb300_moe.h states the formulas).
 //
-// One warp serves one token.  Lane l holds the V = ceil(E / 32) consecutive
-// scores [l V, l V + V) as 32-bit keys whose unsigned order is the scores'
-// order (0 = not choosable), so that the lowest lane and then the lowest slot
-// among equal keys is the lowest expert id.  Each of the K rounds takes the
-// warp's largest key with one redux, finds the first lane that holds it, and
-// that lane drops it.
+// One warp serves one token.  Lane l holds the V = ceil(E / 32) consecutive keys
+// [l V, l V + V) (-inf: not choosable).  Bound by instructions, not by reading the
+// scores, so the K choices are not K searches of the row:
+//   1. the K-th largest of the 32 lane maxima is a bound that at least K keys
+//      reach (one redux.max a step);
+//   2. the keys that reach it -- K and a few, typically -- are gathered into
+//      the first lanes through shared memory;
+//   3. K steps take the largest of one key a lane, the lowest id among equals.
+// Rows where more than 32 keys reach the bound (many equal scores) are searched K
+// times.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
+#include "ep_types.cuh"
 
 namespace epg {
 namespace {
@@ -20,30 +26,20 @@ namespace {
 constexpr int kWarps = 8;
 constexpr unsigned kAll = 0xffffffffu;
 
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <class T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <class T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ float from_float<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
-// Order-preserving key of a score: larger score, larger key; -0 equals +0;
-// 0 for -inf and NaN, which are never chosen.
-__device__ __forceinline__ uint32_t key_of(float z) {
-  const uint32_t u = __float_as_uint(z + 0.0f);
-  const uint32_t k = u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-  return z > -INFINITY ? k : 0u;
+__device__ __forceinline__ T from_float(float v) {
+  if constexpr (sizeof(T) == 4)
+    return v;
+  else
+    return __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -53,7 +49,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // exp(z - peak) for z <= peak; a +inf peak leaves 1 for the +inf scores and 0
-// for the others (the limit).  Masked scores (not > -inf) give 0.
+// for the others (the limit).  Masked scores (-inf) give 0.
 __device__ __forceinline__ float exp_below(float z, float peak) {
   if (!(z > -INFINITY)) return 0.0f;
   return z == peak ? 1.0f : expf(z - peak);
@@ -71,7 +67,7 @@ __device__ __forceinline__ float sigmoid_scaled(float z, float peak) {
   return expf(z - peak) / (1.0f + expf(z));
 }
 
-// The V scores of a lane as floats (-inf past the end of the row).
+// The V scores of a lane as floats; -inf past the end of the row and for NaN.
 template <class T, int V>
 __device__ __forceinline__ void load_row(const T* row, int experts, int lane, bool vec, float (&z)[V]) {
   constexpr int kPer = 16 / sizeof(T);
@@ -83,23 +79,22 @@ __device__ __forceinline__ void load_row(const T* row, int experts, int lane, bo
         const uint4 q = *reinterpret_cast<const uint4*>(row + j0 + v);
         const T* e = reinterpret_cast<const T*>(&q);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) z[v + i] = as_float(e[i]);
+        for (int i = 0; i < kPer; ++i) z[v + i] = fmaxf(as_float(e[i]), -INFINITY);
       }
       return;
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) z[v] = j0 + v < experts ? as_float(row[j0 + v]) : -INFINITY;
+  for (int v = 0; v < V; ++v) z[v] = j0 + v < experts ? fmaxf(as_float(row[j0 + v]), -INFINITY) : -INFINITY;
 }
 
-// Peak of a row (-inf when nothing is choosable) from its lane-held scores.
+// Largest score of a row (-inf when nothing is choosable).
 template <int V>
-__device__ __forceinline__ float row_peak(const float (&z)[V]) {
-  uint32_t m = 0;
+__device__ __forceinline__ float lane_max(const float (&z)[V]) {
+  float m = z[0];
 #pragma unroll
-  for (int v = 0; v < V; ++v) m = max(m, key_of(z[v]));
-  m = __reduce_max_sync(kAll, m);
-  return m ? value_of(m) : -INFINITY;
+  for (int v = 1; v < V; ++v) m = fmaxf(m, z[v]);
+  return m;
 }
 
 template <int V>
@@ -110,61 +105,106 @@ __device__ __forceinline__ float row_exp_sum(const float (&z)[V], float peak) {
   return warp_sum(s);
 }
 
+// Lane k (< topk): the id of the k-th largest key, the lower id first among
+// equals; -1 where fewer keys are above -inf.  `slots`: 32 of the warp's own.
+template <int V>
+__device__ __forceinline__ int choose(float (&key)[V], int topk, int lane, float2* slots) {
+  float val = key[0];
+  int id = lane;
+  if constexpr (V > 1) {
+    float top = lane_max(key), bound = -INFINITY;
+    int k = 0;
+    for (; k < topk; ++k) {
+      const float m = warp_max(top);
+      if (!(m > -INFINITY)) break;
+      bound = m;
+      if (top == m) top = -INFINITY;
+    }
+    // fewer than K lanes hold a key: every key counts
+    const float least = k < topk ? __int_as_float(0xff7fffff) : bound;
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool in = key[v] >= least;
+      const unsigned who = __ballot_sync(kAll, in);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (in && at < 32) slots[at] = make_float2(key[v], __int_as_float(lane * V + v));
+      n += __popc(who);
+    }
+    if (n > 32) {   // more keys than lanes: search the row K times
+      int chosen = -1;
+      for (int i = 0; i < topk; ++i) {
+        float best = -INFINITY;
+        int slot = 0;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+          if (key[v] >= best) best = key[v], slot = v;
+        const float m = warp_max(best);
+        if (!(m > -INFINITY)) break;
+        const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
+        const int j = __shfl_sync(kAll, lane * V + slot, src);
+        if (lane == i) chosen = j;
+        if (lane == src) {
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (v == slot) key[v] = -INFINITY;
+        }
+      }
+      return chosen;
+    }
+    __syncwarp();
+    const float2 mine = slots[lane];
+    val = lane < n ? mine.x : -INFINITY;
+    id = __float_as_int(mine.y);
+  }
+  int chosen = -1;
+  for (int k = 0; k < topk; ++k) {
+    const float m = warp_max(val);
+    if (!(m > -INFINITY)) break;
+    const int j = static_cast<int>(__reduce_min_sync(kAll, val == m ? static_cast<unsigned>(id) : 0xffffffffu));
+    if (lane == k) chosen = j;
+    if (id == j) val = -INFINITY;
+  }
+  return chosen;
+}
+
 template <class T, int V, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteParams p, bool vec) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  __shared__ float2 slots[kWarps][32];
+  allow_dependent_grids();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  grid_dependency_wait();
   if (t >= p.n) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.row_stride;
-  float z[V];
-  load_row<T, V>(row, p.experts, lane, vec, z);
+  float key[V];
+  load_row<T, V>(row, p.experts, lane, vec, key);
   const bool whole = !p.sigmoid && (BIAS || !p.renorm);   // the softmax's full sum is needed
-  const float peak = row_peak(z);
-  const float sum = whole ? row_exp_sum(z, peak) : 1.0f;
-  uint32_t key[V];
+  float peak = 0.0f, sum = 1.0f;
+  if (whole) {
+    peak = warp_max(lane_max(key));
+    sum = row_exp_sum(key, peak);
+  }
+  if constexpr (BIAS) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int j = lane * V + v;
-    if constexpr (BIAS) {
-      const float f = p.sigmoid ? sigmoid(z[v]) : exp_below(z[v], peak) / sum;
-      key[v] = j < p.experts && z[v] > -INFINITY ? key_of(f + p.bias[j]) : 0u;
-    } else {
-      key[v] = key_of(z[v]);
+    for (int v = 0; v < V; ++v) {
+      const int j = lane * V + v;
+      if (key[v] > -INFINITY) {
+        const float f = p.sigmoid ? sigmoid(key[v]) : exp_below(key[v], peak) / sum;
+        key[v] = fmaxf(f + p.bias[j], -INFINITY);
+      }
     }
   }
-  int chosen = -1;                                        // lane k: the k-th expert
-  for (int k = 0; k < p.topk; ++k) {
-    uint32_t best = 0;
-    int slot = 0;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] >= best) best = key[v], slot = v;
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top == 0) break;
-    const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    const int id = __shfl_sync(kAll, lane * V + slot, src);
-    if (lane == k) chosen = id;
-    if (lane == src) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == slot) key[v] = 0;
-    }
-  }
+  const int chosen = choose<V>(key, p.topk, lane, slots[warp]);
   const float zk = chosen >= 0 ? as_float(row[chosen]) : -INFINITY;
   float f;
-  if (p.sigmoid) {
-    // the largest chosen score: with a selection bias not the first one
-    uint32_t m = __reduce_max_sync(kAll, key_of(zk));
-    f = p.renorm ? sigmoid_scaled(zk, m ? value_of(m) : 0.0f) : sigmoid(zk);
-  } else if (p.renorm) {
-    uint32_t m = __reduce_max_sync(kAll, key_of(zk));
-    f = exp_below(zk, m ? value_of(m) : -INFINITY);
-  } else {
-    f = sum > 0.0f ? exp_below(zk, peak) / sum : 0.0f;
-  }
   if (p.renorm) {
+    const float top = warp_max(zk);   // with a selection bias not the first one
+    f = p.sigmoid ? sigmoid_scaled(zk, top) : exp_below(zk, top);
     const float tot = warp_sum(f);
     f = tot > 0.0f ? f / tot : 0.0f;
+  } else {
+    f = p.sigmoid ? sigmoid(zk) : sum > 0.0f ? exp_below(zk, peak) / sum : 0.0f;
   }
   if (lane < p.topk) {
     p.idx[t * p.topk + lane] = chosen;
@@ -172,10 +212,35 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteParams p, bool 
   }
 }
 
+// A lane's V values of an output row.
 template <class T, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams p, bool vec) {
+__device__ __forceinline__ void store_row(T* row, int experts, int lane, bool vec, const float (&z)[V]) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int j0 = lane * V;
+  if constexpr (V % kPer == 0) {
+    if (vec && j0 + V <= experts) {
+#pragma unroll
+      for (int v = 0; v < V; v += kPer) {
+        uint4 q;
+        T* e = reinterpret_cast<T*>(&q);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) e[i] = from_float<T>(z[v + i]);
+        *reinterpret_cast<uint4*>(row + j0 + v) = q;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (j0 + v < experts) row[j0 + v] = from_float<T>(z[v]);
+}
+
+template <class T, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams p, bool vec, bool vec_out) {
+  allow_dependent_grids();
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
   if (t >= p.n) return;
   const T* row = static_cast<const T*>(p.logits) + t * p.row_stride;
   T* out = static_cast<T*>(p.grad) + t * p.grad_stride;
@@ -186,42 +251,38 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams
     if (id < 0 || id >= p.experts) id = -1;
     if (id >= 0) {
       g = p.grad_w[t * p.topk + lane] * p.scale;
-      zk = as_float(row[id]);
+      zk = fmaxf(as_float(row[id]), -INFINITY);
     }
   }
   const bool full = !p.sigmoid && !p.renorm;              // the gradient reaches every expert
-  float d, spread = 0.0f, peak = 0.0f, inv = 0.0f;
+  float z[V], d;
   if (full) {
-    float z[V];
     load_row<T, V>(row, p.experts, lane, vec, z);
-    peak = row_peak(z);
+    const float peak = warp_max(lane_max(z));
     const float sum = row_exp_sum(z, peak);
-    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const float fk = exp_below(zk, peak) * inv;
-    spread = warp_sum(id >= 0 ? g * fk : 0.0f);
+    const float spread = warp_sum(id >= 0 ? g * fk : 0.0f);
     d = fk * (g - spread);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = lane * V + v;
-      if (j < p.experts)
-        out[j] = from_float<T>(z[v] > -INFINITY ? -spread * exp_below(z[v], peak) * inv : 0.0f);
-    }
+    for (int v = 0; v < V; ++v) z[v] = z[v] > -INFINITY ? -spread * exp_below(z[v], peak) * inv : 0.0f;
   } else {
-    for (int j = lane; j < p.experts; j += 32) out[j] = from_float<T>(0.0f);
-    const uint32_t m = __reduce_max_sync(kAll, key_of(zk));
-    const float top = m ? value_of(m) : -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = 0.0f;
     const float s = p.sigmoid ? sigmoid(zk) : 0.0f;
-    float f = !p.renorm ? s : p.sigmoid ? sigmoid_scaled(zk, m ? top : 0.0f) : exp_below(zk, top);
     if (p.renorm) {
+      const float top = warp_max(zk);
+      float f = p.sigmoid ? sigmoid_scaled(zk, top) : exp_below(zk, top);
       const float tot = warp_sum(f);
       f = tot > 0.0f ? f / tot : 0.0f;
       const float mean = warp_sum(id >= 0 ? g * f : 0.0f);
       d = f * (g - mean);
     } else {
-      d = f * g;
+      d = s * g;
     }
     if (p.sigmoid) d *= 1.0f - s;
   }
+  store_row<T, V>(out, p.experts, lane, vec_out, z);
   __syncwarp();                                           // the row's writes come before the K entries'
   if (id >= 0) out[id] = from_float<T>(zk > -INFINITY ? d : 0.0f);
 }
@@ -232,15 +293,22 @@ bool aligned16(const void* p, int64_t stride_bytes) {
 
 template <class T, int V>
 cudaError_t launch_v(const RouteParams& p, bool backward, cudaStream_t s) {
-  const bool vec = aligned16(p.logits, p.row_stride * static_cast<int64_t>(sizeof(T)));
-  const unsigned grid = static_cast<unsigned>((p.n + kWarps - 1) / kWarps);
+  const int64_t size = static_cast<int64_t>(sizeof(T));
+  const bool vec = aligned16(p.logits, p.row_stride * size);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.n + kWarps - 1) / kWarps));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  static const bool pdl = PdlEnabled();
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
   if (backward)
-    route_backward_kernel<T, V><<<grid, kWarps * 32, 0, s>>>(p, vec);
-  else if (p.bias)
-    route_kernel<T, V, true><<<grid, kWarps * 32, 0, s>>>(p, vec);
-  else
-    route_kernel<T, V, false><<<grid, kWarps * 32, 0, s>>>(p, vec);
-  return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, route_backward_kernel<T, V>, p, vec, aligned16(p.grad, p.grad_stride * size));
+  if (p.bias) return cudaLaunchKernelEx(&cfg, route_kernel<T, V, true>, p, vec);
+  return cudaLaunchKernelEx(&cfg, route_kernel<T, V, false>, p, vec);
 }
 
 template <class T>
