@@ -4,7 +4,7 @@
 // One warp serves one token.  Lane l holds the V = ceil(E / 32) consecutive keys
 // [l V, l V + V) (-inf: not choosable).  Bound by instructions, not by reading the
 // scores, so the K choices are not K searches of the row:
-//   1. the K-th largest of the 32 lane maxima is a bound that at least K keys
+//   1. the K-th largest (K rounded up to 8 or 16) of the 32 lane maxima is a bound that at least K keys
 //      reach (one redux.max a step);
 //   2. the keys that reach it -- K and a few, typically -- are gathered into
 //      the first lanes through shared memory;
@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
@@ -97,39 +98,48 @@ __device__ __forceinline__ float lane_max(const float (&z)[V]) {
   return m;
 }
 
+// z becomes exp(z - peak); their sum over the row.
 template <int V>
-__device__ __forceinline__ float row_exp_sum(const float (&z)[V], float peak) {
+__device__ __forceinline__ float exp_row(float (&z)[V], float peak) {
   float s = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) s += exp_below(z[v], peak);
+  for (int v = 0; v < V; ++v) {
+    z[v] = exp_below(z[v], peak);
+    s += z[v];
+  }
   return warp_sum(s);
 }
 
-// Lane k (< topk): the id of the k-th largest key, the lower id first among
-// equals; -1 where fewer keys are above -inf.  `slots`: 32 of the warp's own.
-template <int V>
-__device__ __forceinline__ int choose(float (&key)[V], int topk, int lane, float2* slots) {
+// Lane k (< topk <= KT): the id of the k-th largest key, the lower id first among
+// equals, and the key; -1 and -inf where fewer keys are above -inf.  key_of(id)
+// gives any key of the row, `slots` are 32 of the warp's own.  The steps are KT
+// whatever topk is, so that they unroll: more of them only lower the bound and fill
+// lanes that nobody reads.
+template <int V, int KT, class KeyOf>
+__device__ __forceinline__ int choose(float (&key)[V], int topk, int lane, int* slots, KeyOf key_of, float& chosen_key) {
   float val = key[0];
   int id = lane;
   if constexpr (V > 1) {
-    float top = lane_max(key), bound = -INFINITY;
-    int k = 0;
-    for (; k < topk; ++k) {
-      const float m = warp_max(top);
-      if (!(m > -INFINITY)) break;
-      bound = m;
-      if (top == m) top = -INFINITY;
-    }
-    // fewer than K lanes hold a key: every key counts
-    const float least = k < topk ? __int_as_float(0xff7fffff) : bound;
-    int n = 0;
+    float top = lane_max(key), bound = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool in = key[v] >= least;
-      const unsigned who = __ballot_sync(kAll, in);
-      const int at = n + __popc(who & ((1u << lane) - 1u));
-      if (in && at < 32) slots[at] = make_float2(key[v], __int_as_float(lane * V + v));
-      n += __popc(who);
+    for (int k = 0; k < KT; ++k) {
+      bound = warp_max(top);
+      if (top == bound) top = -INFINITY;
+    }
+    // -inf where fewer than KT lanes hold a key: then every key counts
+    bound = fmaxf(bound, __int_as_float(0xff7fffff));
+    using Mask = std::conditional_t<(V > 32), uint64_t, uint32_t>;
+    Mask mine = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (key[v] >= bound) mine |= Mask{1} << v;
+    int n = 0;
+    const unsigned below = (1u << lane) - 1u;
+    // lanes with more to give: two or three turns for the usual K and a few keys
+    for (unsigned who; n <= 32 && (who = __ballot_sync(kAll, mine != 0)) != 0; n += __popc(who)) {
+      const int at = n + __popc(who & below);
+      if (mine != 0 && at < 32) slots[at] = lane * V + (V > 32 ? __ffsll(static_cast<long long>(mine)) : __ffs(static_cast<int>(mine))) - 1;
+      mine &= mine - 1;
     }
     if (n > 32) {   // more keys than lanes: search the row K times
       int chosen = -1;
@@ -143,7 +153,7 @@ __device__ __forceinline__ int choose(float (&key)[V], int topk, int lane, float
         if (!(m > -INFINITY)) break;
         const int src = __ffs(__ballot_sync(kAll, best == m)) - 1;
         const int j = __shfl_sync(kAll, lane * V + slot, src);
-        if (lane == i) chosen = j;
+        if (lane == i) chosen = j, chosen_key = m;
         if (lane == src) {
 #pragma unroll
           for (int v = 0; v < V; ++v)
@@ -153,24 +163,24 @@ __device__ __forceinline__ int choose(float (&key)[V], int topk, int lane, float
       return chosen;
     }
     __syncwarp();
-    const float2 mine = slots[lane];
-    val = lane < n ? mine.x : -INFINITY;
-    id = __float_as_int(mine.y);
+    id = lane < n ? slots[lane] : -1;
+    val = lane < n ? key_of(id) : -INFINITY;
   }
   int chosen = -1;
-  for (int k = 0; k < topk; ++k) {
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
     const float m = warp_max(val);
-    if (!(m > -INFINITY)) break;
     const int j = static_cast<int>(__reduce_min_sync(kAll, val == m ? static_cast<unsigned>(id) : 0xffffffffu));
-    if (lane == k) chosen = j;
+    if (lane == k) chosen = j, chosen_key = m;
     if (id == j) val = -INFINITY;
   }
+  if (lane >= topk || !(chosen_key > -INFINITY)) chosen = -1, chosen_key = -INFINITY;
   return chosen;
 }
 
-template <class T, int V, bool BIAS>
+template <class T, int V, int KT, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteParams p, bool vec) {
-  __shared__ float2 slots[kWarps][32];
+  __shared__ int slots[kWarps][32];
   allow_dependent_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -183,20 +193,29 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteParams p, bool 
   float peak = 0.0f, sum = 1.0f;
   if (whole) {
     peak = warp_max(lane_max(key));
-    sum = row_exp_sum(key, peak);
+    float e[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = key[v];
+    sum = exp_row(e, peak);
   }
+  auto biased = [&](float z, int j) {
+    const float f = p.sigmoid ? sigmoid(z) : exp_below(z, peak) / sum;
+    return z > -INFINITY ? fmaxf(f + p.bias[j], -INFINITY) : -INFINITY;
+  };
   if constexpr (BIAS) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = lane * V + v;
-      if (key[v] > -INFINITY) {
-        const float f = p.sigmoid ? sigmoid(key[v]) : exp_below(key[v], peak) / sum;
-        key[v] = fmaxf(f + p.bias[j], -INFINITY);
-      }
-    }
+    for (int v = 0; v < V; ++v)
+      if (lane * V + v < p.experts) key[v] = biased(key[v], lane * V + v);
   }
-  const int chosen = choose<V>(key, p.topk, lane, slots[warp]);
-  const float zk = chosen >= 0 ? as_float(row[chosen]) : -INFINITY;
+  float zk = -INFINITY;
+  const int chosen = choose<V, KT>(
+      key, p.topk, lane, slots[warp],
+      [&](int j) {
+        const float z = fmaxf(as_float(row[j]), -INFINITY);
+        return BIAS ? biased(z, j) : z;
+      },
+      zk);
+  if constexpr (BIAS) zk = chosen >= 0 ? as_float(row[chosen]) : -INFINITY;
   float f;
   if (p.renorm) {
     const float top = warp_max(zk);   // with a selection bias not the first one
@@ -259,13 +278,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams
   if (full) {
     load_row<T, V>(row, p.experts, lane, vec, z);
     const float peak = warp_max(lane_max(z));
-    const float sum = row_exp_sum(z, peak);
+    const float sum = exp_row(z, peak);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     const float fk = exp_below(zk, peak) * inv;
     const float spread = warp_sum(id >= 0 ? g * fk : 0.0f);
     d = fk * (g - spread);
 #pragma unroll
-    for (int v = 0; v < V; ++v) z[v] = z[v] > -INFINITY ? -spread * exp_below(z[v], peak) * inv : 0.0f;
+    for (int v = 0; v < V; ++v) z[v] = z[v] > 0.0f ? -spread * z[v] * inv : 0.0f;
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) z[v] = 0.0f;
@@ -307,8 +326,11 @@ cudaError_t launch_v(const RouteParams& p, bool backward, cudaStream_t s) {
   cfg.numAttrs = pdl ? 1 : 0;
   if (backward)
     return cudaLaunchKernelEx(&cfg, route_backward_kernel<T, V>, p, vec, aligned16(p.grad, p.grad_stride * size));
-  if (p.bias) return cudaLaunchKernelEx(&cfg, route_kernel<T, V, true>, p, vec);
-  return cudaLaunchKernelEx(&cfg, route_kernel<T, V, false>, p, vec);
+  if (p.topk <= 8)
+    return p.bias ? cudaLaunchKernelEx(&cfg, route_kernel<T, V, 8, true>, p, vec)
+                  : cudaLaunchKernelEx(&cfg, route_kernel<T, V, 8, false>, p, vec);
+  return p.bias ? cudaLaunchKernelEx(&cfg, route_kernel<T, V, 16, true>, p, vec)
+                : cudaLaunchKernelEx(&cfg, route_kernel<T, V, 16, false>, p, vec);
 }
 
 template <class T>
