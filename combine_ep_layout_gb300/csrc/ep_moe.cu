@@ -24,10 +24,12 @@
 // down product whose sums are added: a column costs nothing until 4 tokens meet
 // on an expert, and the rounding of h to 8 bits would double the output's error.
 //
-// The down items write fp32 expert rows; the block that finishes the last round of
-// a channel tile folds the K rows of each token in order (fmaf over k, as the
-// combine does) once its own items are done.  No sum depends on the order of
-// blocks: equal inputs, equal bits.
+// The down items write fp32 expert rows.  A block that is through with its items
+// waits for the rounds of its share of the channel tiles and folds the K rows of
+// each token there in order (fmaf over k, as the combine does); every block has the
+// same share, whichever was late (folded by the block that finished a tile last, 64
+// tokens' rows took the latest block 120 us).  No sum depends on the order of blocks:
+// equal inputs, equal bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -89,6 +91,21 @@ constexpr int kQueue = 64;
 __device__ __forceinline__ int red_8(int row, int col) { return row * 8 + (col ^ (row >> 1 & 6)); }
 __device__ __forceinline__ int red_4(int row, int tok) { return row * 4 + (tok ^ (row >> 3 & 3)); }
 
+// Until the counter that other blocks raise is at `want`.  Gives up after wait_ns
+// (or at once where another wait of the block gave up): the launch goes on, in
+// bounds, and reports that its output is not valid.
+__device__ __forceinline__ void await_global(const int32_t* counter, int want, uint64_t wait_ns, int* lost, int32_t* err) {
+  if (load_acquire(counter) >= want || *static_cast<volatile int*>(lost)) return;
+  const uint64_t t0 = now_ns();
+  while (load_acquire(counter) < want) {
+    if (now_ns() - t0 > wait_ns) {
+      *static_cast<volatile int*>(lost) = 1;
+      atomicOr(err, kErrTimeout);
+      return;
+    }
+  }
+}
+
 // Until *count >= want, a count in shared memory that another warp raises; gives
 // up (false) after the clean-up limit.
 __device__ __forceinline__ bool await_count(const int* count, int want) {
@@ -125,9 +142,6 @@ struct Lists {
 };
 
 constexpr int lists_bytes(int entries) { return (entries * (4 + 4 + 2) + entries / 8 + 4 + 15) & ~15; }
-// Channel tiles of the down product that one block may have to fold: at most
-// every tile (hidden_dim <= 32768 over 32 channels).
-constexpr int kMaxTiles = 1024;
 
 // How a block is cut for weights of form G and up to NT column tiles a job.  The
 // ring takes what shared memory is left; 64 KB of weights under way per SM carry
@@ -151,8 +165,8 @@ struct Shape {
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr int kRing = kWarps * kStages * kSlot;
   static_assert(kStages >= 2);
-  // the expert counts of the set-up (2048 x 4 bytes) and the ranks use the ring
-  static_assert(kRing >= 4 * 2048 + 4 * kMaxEntries);
+  // the set-up's counts (of 2048 experts, 32 bytes and a word each) and ranks use the ring
+  static_assert(kRing >= 2048 * 36 + 4 * kMaxEntries);
 };
 
 template <int G, int NT>
@@ -163,11 +177,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   constexpr int kThreads = S::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t scan_warp[kAllWarps];
-  __shared__ int s_flag, s_lost, s_rounds, s_finished;
+  __shared__ int s_flag, s_lost, s_rounds;
   __shared__ __align__(8) uint64_t s_free[2];
   __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
   __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
-  __shared__ uint16_t finished[kMaxTiles];   // the tiles this block folds
   allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int entries = p.n * p.topk;
@@ -182,36 +195,45 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   }
 
   // ---- which experts, with which tokens: every block works it out for itself
-  int* count = reinterpret_cast<int*>(smem);                              // by expert
-  uint16_t* expert_of = reinterpret_cast<uint16_t*>(smem + 4 * 2048);     // by entry
-  uint16_t* rank_of = expert_of + kMaxEntries;
+  // Entries go by chunks of 32, a warp each, in any order: what an entry's place
+  // among its expert's needs is how many of the expert's entries earlier chunks have,
+  // one byte for each expert and chunk.
+  uint32_t* by_chunk = reinterpret_cast<uint32_t*>(smem);                 // [E][32 bytes]
+  int* first_of = reinterpret_cast<int*>(smem + 2048 * 32);               // by expert
+  uint16_t* expert_of = reinterpret_cast<uint16_t*>(smem + 2048 * 36);    // by entry
+  uint16_t* rank_of = expert_of + kMaxEntries;                            // within its chunk
+  const int chunk_words = (entries + 127) / 128;                          // of 4 bytes
+  auto entries_before = [&](int e, int chunk) {
+    int sum = 0;
+    for (int w = 0; 4 * w < chunk; ++w) {
+      const int bytes = chunk - 4 * w;
+      const uint32_t mask = bytes >= 4 ? ~0u : (1u << 8 * bytes) - 1u;
+      sum = static_cast<int>(__dp4a(by_chunk[8 * e + w] & mask, 0x01010101u, static_cast<unsigned>(sum)));
+    }
+    return sum;
+  };
   if (tid == 0) {
-    s_lost = s_rounds = s_finished = s_written[0] = s_written[1] = s_told = 0;
+    s_lost = s_rounds = s_written[0] = s_written[1] = s_told = 0;
     for (int b = 0; b < 2; ++b) tma::mbar_init(stream::smem_addr(&s_free[b]), 1);
   }
   const uint32_t free_bar = stream::smem_addr(s_free);
-  for (int e = tid; e < p.experts; e += kThreads) count[e] = 0;
+  for (int i = tid; i < p.experts * chunk_words; i += kThreads) by_chunk[i / chunk_words * 8 + i % chunk_words] = 0;
   __syncthreads();
   grid_dependency_wait();   // no memory of the device has been touched before this
-  if (warp == 0) {   // one warp in entry order: the order within an expert is the same in every block
-    for (int i0 = 0; i0 < entries; i0 += 32) {
-      const int i = i0 + lane;
-      int64_t id = -1;
-      if (i < entries) id = p.topk_idx[i];
-      const bool ok = id >= 0 && id < p.experts;
-      if (i < entries && !ok && id != -1 && blockIdx.x == 0) atomicOr(p.err, kErrBadExpert);
-      const int e = ok ? static_cast<int>(id) : -1 - lane;
-      const unsigned same = __match_any_sync(kAll, e);
-      const unsigned oks = __ballot_sync(kAll, ok);
-      const int before = ok ? count[e] : 0;
-      __syncwarp();
-      if (ok && (same >> lane) == 1u) count[e] = before + __popc(same);   // the last of the equal ones
-      __syncwarp();
-      if (lane == 0) L.valid[i0 / 32] = oks;
-      if (i < entries) {
-        expert_of[i] = ok ? static_cast<uint16_t>(e) : 0xffff;
-        rank_of[i] = static_cast<uint16_t>(before + __popc(same & ((1u << lane) - 1u)));
-      }
+  for (int i0 = 32 * warp; i0 < entries; i0 += kThreads) {
+    const int i = i0 + lane;
+    int64_t id = -1;
+    if (i < entries) id = p.topk_idx[i];
+    const bool ok = id >= 0 && id < p.experts;
+    if (i < entries && !ok && id != -1 && blockIdx.x == 0) atomicOr(p.err, kErrBadExpert);
+    const int e = ok ? static_cast<int>(id) : -1 - lane;
+    const unsigned same = __match_any_sync(kAll, e), before = same & ((1u << lane) - 1u);
+    const unsigned oks = __ballot_sync(kAll, ok);
+    if (ok && before == 0) reinterpret_cast<uint8_t*>(by_chunk)[32 * e + i0 / 32] = static_cast<uint8_t>(__popc(same));
+    if (lane == 0) L.valid[i0 / 32] = oks;
+    if (i < entries) {
+      expert_of[i] = ok ? static_cast<uint16_t>(e) : 0xffff;
+      rank_of[i] = static_cast<uint16_t>(__popc(before));
     }
   }
   __syncthreads();
@@ -227,7 +249,11 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     };
     uint64_t mine = 0;
     int rounds = 0;        // down rounds of one channel tile
-    for (int e = e0; e < e1; ++e) mine += word(count[e]), rounds += (count[e] + 3) >> 2;
+    for (int e = e0; e < e1; ++e) {
+      const int c = entries_before(e, 4 * chunk_words);
+      first_of[e] = c;
+      mine += word(c), rounds += (c + 3) >> 2;
+    }
     if (rounds) atomicAdd(&s_rounds, rounds);
     uint64_t upto = mine;
 #pragma unroll
@@ -245,7 +271,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     jobs_0 = static_cast<int>(all >> 16 & 0xffff);
     jobs_1 = static_cast<int>(all >> 32 & 0xffff);
     for (int e = e0; e < e1; ++e) {
-      const int c = count[e];
+      const int c = first_of[e];
       if (c == 0) continue;
       const int start = static_cast<int>(base & 0xffff);
       for (int ph = 0; ph < 2; ++ph) {
@@ -255,14 +281,14 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
           (ph == 0 ? L.jobs_0 : L.jobs_1)[j] = pack_job(e, start + o, min(cap, c - o), (c + 7) >> 3);
       }
       base += word(c);
-      count[e] = start;
+      first_of[e] = start;
     }
   }
   __syncthreads();
   for (int i = tid; i < entries; i += kThreads) {
     const int e = expert_of[i];
     if (e != 0xffff) {
-      L.entry[count[e] + rank_of[i]] = static_cast<uint16_t>(i);
+      L.entry[first_of[e] + entries_before(e, i / 32) + rank_of[i]] = static_cast<uint16_t>(i);
     }
   }
   __syncthreads();   // the ring's memory is free from here on
@@ -428,20 +454,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       if (col < x_cols) stream::copy16(slot + F::x_offset(col, lane_xpiece), src + x_off[i], ok);
     }
   };
-  // until every gate/up item of the job's expert is done; gives up after wait_ns
+  // until every gate/up item of the job's expert is done
   auto await_expert = [&](const Walk& w) {
     const Job job = job_at(1, w.job);
-    const int want = tiles_0 * job.parts;
-    if (lane == 0 && load_acquire(p.ready + job.expert) < want && !*static_cast<volatile int*>(&s_lost)) {
-      const uint64_t t0 = now_ns();
-      while (load_acquire(p.ready + job.expert) < want) {
-        if (now_ns() - t0 > p.wait_ns) {
-          *static_cast<volatile int*>(&s_lost) = 1;
-          atomicOr(p.err, kErrTimeout);
-          break;
-        }
-      }
-    }
+    if (lane == 0) await_global(p.ready + job.expert, tiles_0 * job.parts, p.wait_ns, &s_lost, p.err);
     __syncwarp();
   };
 
@@ -534,15 +550,15 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             float* r0 = red + warp * F::kRows * 8;
-            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g, 2 * t)) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
-            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g + 8, 2 * t)) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g, 2 * t)) = make_float2(acc[rt][nt][0] * F::kOut, acc[rt][nt][1] * F::kOut);
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g + 8, 2 * t)) = make_float2(acc[rt][nt][2] * F::kOut, acc[rt][nt][3] * F::kOut);
           }
         } else {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             float* r0 = red + warp * F::kRows * 4;
-            r0[red_4(16 * rt + g, t)] = acc[rt][nt][0] + acc[rt][nt][1];
-            r0[red_4(16 * rt + g + 8, t)] = acc[rt][nt][2] + acc[rt][nt][3];
+            r0[red_4(16 * rt + g, t)] = (acc[rt][nt][0] + acc[rt][nt][1]) * F::kOut;
+            r0[red_4(16 * rt + g + 8, t)] = (acc[rt][nt][2] + acc[rt][nt][3]) * F::kOut;
           }
         }
         bar_arrive<32 * (kWarps + 1)>(kBarFull + buf);
@@ -620,7 +636,6 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     }
   } else {
     // ---- the warp that tells: rounds [told, upto) are written, one fence for all of them
-    const int rounds_1 = s_rounds;
     int total[2] = {0, 0};
     for (int ph = 0; ph < 2; ++ph) {
       int job_i = 0, tile = first(ph);
@@ -642,48 +657,60 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       const int r = __shfl_sync(kAll, told, 0) + lane;
       if (r < __shfl_sync(kAll, upto, 0)) {
         const int what = *static_cast<volatile uint16_t*>(&queue[r % kQueue]);
-        if (r < total[0])
-          atomicAdd(p.ready + what, 1);
-        else if (atomicAdd(p.tile_done + what, 1) == rounds_1 - 1)
-          finished[atomicAdd(&s_finished, 1)] = static_cast<uint16_t>(what);
+        atomicAdd(r < total[0] ? p.ready + what : p.tile_done + what, 1);
       }
       told = __shfl_sync(kAll, upto, 0);
       if (lane == 0) *static_cast<volatile int*>(&s_told) = told;
     }
   }
-  __threadfence();
-  __syncthreads();         // `finished` is complete
+  // ---- this block's share of the channel tiles: the K rows of each token
+  const int my_tiles = blockIdx.x < tiles_1 ? (tiles_1 - 1 - static_cast<int>(blockIdx.x)) / grid + 1 : 0;
+  for (int f = tid; f < my_tiles; f += kThreads)
+    await_global(p.tile_done + blockIdx.x + f * grid, s_rounds, p.wait_ns, &s_lost, p.err);
+  __syncthreads();
   {
-    const int n_done = s_finished, rows = F::kRows << side_1;
-    for (int f = 0; f < n_done; ++f) {
-      for (int v = tid; v < rows * p.n; v += kThreads) {
-        const int tok = v / F::kRows >> side_1, c = finished[f] * rows + (v & (rows - 1));
-        if (c >= p.hidden) continue;
-        float sum = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < p.topk; ++k) {
-          const int en = tok * p.topk + k;
-          const float y = __ldcg(p.part + static_cast<int64_t>(en) * p.hidden + c);
-          if (L.valid[en / 32] >> (en % 32) & 1) sum = fmaf(p.topk_weights[en], y, sum);
-        }
-        const int64_t o = static_cast<int64_t>(tok) * p.hidden + c;
-        if (p.bias) sum += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[o]);
-        if (p.out_f32)
-          static_cast<float*>(p.out)[o] = sum;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(sum);
+    // four channels at a time, two of them in flight a thread and step of k
+    const int rows = F::kRows << side_1, quads = rows / 4, per_tile = quads * p.n, total = my_tiles * per_tile;
+    for (int v0 = tid; v0 < total; v0 += 2 * kThreads) {
+      float4 sum[2];
+      int tok[2], c[2];        // c < 0: no value
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int v = min(v0 + i * kThreads, total - 1), f = v / per_tile, w = v - f * per_tile;
+        tok[i] = w / quads;
+        c[i] = (static_cast<int>(blockIdx.x) + f * grid) * rows + 4 * (w - tok[i] * quads);
+        if (v0 + i * kThreads >= total || c[i] >= p.hidden) c[i] = -1;
+        sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
-    }
-  }
-  stream::wait<0>();
-  if (jobs_1 == 0) {   // every entry masked
-    const int64_t total = static_cast<int64_t>(p.n) * p.hidden;
-    for (int64_t o = static_cast<int64_t>(blockIdx.x) * kThreads + tid; o < total; o += static_cast<int64_t>(grid) * kThreads) {
-      const float v = p.bias ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[o]) : 0.0f;
-      if (p.out_f32)
-        static_cast<float*>(p.out)[o] = v;
-      else
-        static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+#pragma unroll 4
+      for (int k = 0; k < p.topk; ++k) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int en = tok[i] * p.topk + k;
+          if (c[i] < 0 || !(L.valid[en / 32] >> (en % 32) & 1)) continue;
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(en) * p.hidden + c[i]));
+          const float w = p.topk_weights[en];
+          sum[i].x = fmaf(w, y.x, sum[i].x), sum[i].y = fmaf(w, y.y, sum[i].y);
+          sum[i].z = fmaf(w, y.z, sum[i].z), sum[i].w = fmaf(w, y.w, sum[i].w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (c[i] < 0) continue;
+        const int64_t o = static_cast<int64_t>(tok[i]) * p.hidden + c[i];
+        if (p.bias) {
+          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.bias) + o);
+          sum[i].x += __uint_as_float(b.x << 16), sum[i].y += __uint_as_float(b.x & 0xffff0000u);
+          sum[i].z += __uint_as_float(b.y << 16), sum[i].w += __uint_as_float(b.y & 0xffff0000u);
+        }
+        if (p.out_f32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = sum[i];
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[i].x, sum[i].y), hi = __floats2bfloat162_rn(sum[i].z, sum[i].w);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      }
     }
   }
   // the last block to get here clears the counters for the next launch

@@ -67,14 +67,26 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Two of a word's nibbles (bits 0-3 and 16-19 of v) as bf16 values nibble - 8:
-// with 0x43 above it a nibble reads as the bf16 128 + nibble, exactly.
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t v) {
-  uint32_t u;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(u) : "r"(v));
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                   __nv_bfloat162(__float2bfloat16(136.0f), __float2bfloat16(136.0f)));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Nibbles as bf16 operands without arithmetic.  The bf16 codes 0 to 255 are the
+// values code * 2^-133 (subnormals, and the first binade goes on at their spacing),
+// and the matrix instruction takes them as such.  So a nibble q in bits 0-3 of a
+// half word is already q * 2^-133, and one in bits 4-7 is 16 q * 2^-133: masks and
+// one shift make the operands of eight weights.  The activations carry the rest:
+// times 2^64, the odd columns (bits 4-7) times 2^60, exact in bf16 for magnitudes
+// below 2^64 (a larger one counts as infinite).  The offset of 8 is a product too:
+// a row of -8 for every column, the same for all rows, added to each group's sums
+// before its scale.  (Making q - 8 by or-ing an exponent and subtracting took 11
+// instructions for the 5 here, on the pipe that bounds these kernels.)
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
+constexpr float kUnit = 590295810358705651712.0f;   // 2^69: what sums of such products are to be multiplied by
+
+// Two neighbouring activations (even and odd column) as operands.
+__device__ __forceinline__ uint32_t lift(uint32_t x) {
+  const uint32_t by = 0x5d805f80u;                  // 2^60 (odd), 2^64 (even)
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
+  return r;
 }
 
 // G: 0 for bf16 weights, else the group size of the 4-bit form.  RT: row tiles of 16.
@@ -96,6 +108,8 @@ struct Form {
 
   static constexpr int stage_bytes(int nt) { return kABytes + kSBytes + 8 * nt * kXBytes; }
 
+  static constexpr float kOut = kInt4 ? kUnit : 1.0f;     // what sums are to be multiplied by
+
   // Where piece c of weight row r lies in a stage: the 8 rows that a quarter
   // of the reading lanes touch fall on different banks.
   __device__ static __forceinline__ uint32_t a_offset(int r, int c) {
@@ -109,7 +123,7 @@ struct Form {
   __device__ static __forceinline__ uint32_t x_offset(int col, int c) { return kABytes + kSBytes + x_at(col, c); }
 };
 
-// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
+// acc[rt][nt] += (in units of 2^-69 for 4-bit weights) tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
 // and scales at `slot`, columns at `cols`.
 template <int G, int RT, int NT, int CAP>
 __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* cols, int lane, float (&acc)[RT][CAP][4]) {
@@ -117,7 +131,7 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
   const int g = lane >> 2, t = lane & 3;
   if constexpr (!F::kInt4) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
+    for (int kk = 0; kk < F::kCols / 32; ++kk) {
       uint4 lo[F::kRowTiles], hi[F::kRowTiles];
 #pragma unroll
       for (int rt = 0; rt < F::kRowTiles; ++rt) {
@@ -139,31 +153,37 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
     // nibble i + 4, and the activations are paired the same way.
 #pragma unroll
     for (int grp = 0; grp < F::kScales; ++grp) {
-      float sum[F::kRowTiles][NT][4];
+      float sum[F::kRowTiles][NT][4], offset[NT][4];
 #pragma unroll
       for (int q = grp * (G / 32); q < (grp + 1) * (G / 32); ++q) {
+        const bool first = q == grp * (G / 32);
         uint32_t b[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
+          uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
+          x.x = lift(x.x), x.y = lift(x.y), x.z = lift(x.z), x.w = lift(x.w);
           b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
           b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
           b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
           b[nt][3] = __byte_perm(x.y, x.w, 0x7632);
+          if (first)
+            mma_first(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
+          else
+            mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
+          mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][2], b[nt][3]);
         }
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
           const uint32_t lo = load4(slot + F::a_offset(16 * rt + g, q) + 4 * t);
           const uint32_t hi = load4(slot + F::a_offset(16 * rt + g + 8, q) + 4 * t);
-          const uint32_t a[8] = {nibble_pair(lo),      nibble_pair(hi),      nibble_pair(lo >> 4),  nibble_pair(hi >> 4),
-                                 nibble_pair(lo >> 8), nibble_pair(hi >> 8), nibble_pair(lo >> 12), nibble_pair(hi >> 12)};
+          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            if (q == grp * (G / 32))
-              mma_first(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+            if (first)
+              mma_first(sum[rt][nt], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, b[nt][0], b[nt][1]);
             else
-              mma(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
-            mma(sum[rt][nt], a[4], a[5], a[6], a[7], b[nt][2], b[nt][3]);
+              mma(sum[rt][nt], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, b[nt][0], b[nt][1]);
+            mma(sum[rt][nt], lo8 & kLow, hi8 & kLow, lo8 & kHigh, hi8 & kHigh, b[nt][2], b[nt][3]);
           }
         }
       }
@@ -173,10 +193,10 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
         const float s1 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          acc[rt][nt][0] = fmaf(s0, sum[rt][nt][0], acc[rt][nt][0]);
-          acc[rt][nt][1] = fmaf(s0, sum[rt][nt][1], acc[rt][nt][1]);
-          acc[rt][nt][2] = fmaf(s1, sum[rt][nt][2], acc[rt][nt][2]);
-          acc[rt][nt][3] = fmaf(s1, sum[rt][nt][3], acc[rt][nt][3]);
+          acc[rt][nt][0] = fmaf(s0, sum[rt][nt][0] + offset[nt][0], acc[rt][nt][0]);
+          acc[rt][nt][1] = fmaf(s0, sum[rt][nt][1] + offset[nt][1], acc[rt][nt][1]);
+          acc[rt][nt][2] = fmaf(s1, sum[rt][nt][2] + offset[nt][2], acc[rt][nt][2]);
+          acc[rt][nt][3] = fmaf(s1, sum[rt][nt][3] + offset[nt][3], acc[rt][nt][3]);
         }
       }
     }

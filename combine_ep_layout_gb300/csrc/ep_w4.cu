@@ -86,7 +86,7 @@ __device__ __forceinline__ void put_sums(float* red, int row0, int lane, const f
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        red[sum_at<ROWS>(row0 + 16 * rt + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1))] = acc[rt][nt][i];
+        red[sum_at<ROWS>(row0 + 16 * rt + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1))] = acc[rt][nt][i] * stream::kUnit;
 }
 
 // ------------------------------------------------------------------ narrow
