@@ -155,7 +155,7 @@ struct Shape {
   static constexpr int kCap0 = 8 * NT, kCap1 = 4 * NT;
   static constexpr int kEnough = 8, kItems = 4;              // stages of a warp in an item, items of a block (see widen)
   using F = Form<G, kRowTiles>;
-  static constexpr int kWarps = G != 0 && NT == 1 ? 12 : 8;
+  static constexpr int kWarps = G != 0 ? 12 : 8;
   static constexpr int kAllWarps = kWarps + kFinishers + 1;
   static constexpr int kThreads = 32 * kAllWarps;
   static constexpr int kTokens = NT == 1 ? 8 : kFewTokens;   // most tokens of a call
@@ -317,9 +317,31 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   auto jobs_of = [&](int ph) { return pick(ph, jobs_0, jobs_1); };
   auto job_at = [&](int ph, int j) { return unpack_job(pick(ph, L.jobs_0, L.jobs_1)[j]); };
   const uint32_t by_topk = 65536u / static_cast<uint32_t>(p.topk) + 1;    // entry / topk, exact below 2^14
-  // this block's first item of each phase: the down items go on where the gate/up items ended
-  const int first_1 = (static_cast<int>(blockIdx.x) - jobs_0 * tiles_0 % grid + grid) % grid;
-  auto first = [&](int ph) { return pick(ph, static_cast<int>(blockIdx.x), first_1); };
+  // This block's items, phase by phase: every grid-th of the list, but where the
+  // gate/up items do not go round evenly, the blocks with one fewer (`late` on) take
+  // the first `extra` rounds of down items among themselves, as many as weigh what a
+  // gate/up item does.
+  const int late = jobs_0 * tiles_0 % grid, lates = grid - late;
+  const int extra = late == 0 ? 0
+                              : min((2 * (p.hidden << side_0) / (p.inter << side_1) + 1) / 2, jobs_1 * tiles_1 / lates);
+  const int block = static_cast<int>(blockIdx.x), my_extra = block >= late ? extra : 0;
+  struct Items {
+    int ph, job, tile, n;   // the n-th of this block in phase ph
+  };
+  auto settle_tile = [&](Items& i) {
+    while (i.tile >= tiles(i.ph)) i.tile -= tiles(i.ph), ++i.job;
+  };
+  auto begin_items = [&](Items& i, int ph) {
+    i = {ph, 0, block, 0};
+    if (ph == 1) i.tile = my_extra > 0 ? block - late : extra * lates + block;
+    if (ph < 2) settle_tile(i);
+  };
+  auto next_item = [&](Items& i) {
+    ++i.n;
+    i.tile += i.ph == 0 || i.n > my_extra ? grid : i.n < my_extra ? lates : lates + late;
+    settle_tile(i);
+  };
+  auto there = [&](const Items& i) { return i.job < jobs_of(i.ph); };
 
   if (warp < kWarps) {   // ---- the streaming warps
   const uint32_t ring = stream::smem_addr(smem) + warp * kStages * S::kSlot;
@@ -334,21 +356,23 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   auto step = [&](int ph) { return pick(ph, step_0, step_1); };
   auto lead = [&](int ph) { return pick(ph, lead_0, lead_1); };
   auto sub_tile = [&](int ph, int tile) { return pick(ph, (tile << side_0) + at_0, (tile << side_1) + at_1); };
-  struct Walk {
-    int ph, job, tile, c;
+  struct Walk : Items {
+    int c;
   };
-  auto begin = [&](Walk& w, int ph) { w = {ph, 0, pick(ph, first(0), first(1)), ph < 2 ? lead(ph) : 0}; };
-  // to an item where this warp has a chunk: over the ends of items, jobs and phases
+  auto begin = [&](Walk& w, int ph) {
+    begin_items(w, ph);
+    w.c = ph < 2 ? lead(ph) : 0;
+  };
+  // to an item where this warp has a chunk: over the ends of items and phases
   auto settle = [&](Walk& w) {
     while (w.ph < 2) {
-      while (w.tile >= tiles(w.ph)) w.tile -= tiles(w.ph), ++w.job;
-      if (w.job >= jobs_of(w.ph)) {
+      if (!there(w)) {
         begin(w, w.ph + 1);
       } else if (w.c < chunks(w.ph)) {
         return;
       } else {
         w.c -= chunks(w.ph);
-        w.tile += grid;
+        next_item(w);
       }
     }
   };
@@ -510,11 +534,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       stream::wait<0>();
       __syncwarp();
     }
-    int job_i = 0, tile = first(phase), c = lead(phase);
-    for (;; tile += grid) {
-      while (tile >= tiles(phase)) tile -= tiles(phase), ++job_i;
-      if (job_i >= jobs_of(phase)) break;
-      const Job job = job_at(phase, job_i);
+    Items item;
+    int c = lead(phase);
+    for (begin_items(item, phase); there(item); next_item(item)) {
+      const Job job = job_at(phase, item.job);
       const int cols = phase == 0 ? job.count : 2 * job.count;
       const int nts = (cols + 7) >> 3;
       float acc[RT][NT][4];
@@ -585,11 +608,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     };
     for (int phase = 0; phase < 2; ++phase) {
       const int step = kWarps >> pick(phase, side_0, side_1);
-      int job_i = 0, tile = first(phase);
-      for (;; tile += grid) {
-        while (tile >= tiles(phase)) tile -= tiles(phase), ++job_i;
-        if (job_i >= jobs_of(phase)) break;
-        const Job job = job_at(phase, job_i);
+      Items item;
+      for (begin_items(item, phase); there(item); next_item(item)) {
+        const Job job = job_at(phase, item.job);
+        const int tile = item.tile;
         const int cols = pick(phase, 1, 2) * job.count;
         for (int nt = 0; 8 * nt < cols; ++nt, ++round) {
           if ((round & 1) != buf) continue;
@@ -638,11 +660,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     // ---- the warp that tells: rounds [told, upto) are written, one fence for all of them
     int total[2] = {0, 0};
     for (int ph = 0; ph < 2; ++ph) {
-      int job_i = 0, tile = first(ph);
-      for (;; tile += grid) {
-        while (tile >= tiles(ph)) tile -= tiles(ph), ++job_i;
-        if (job_i >= jobs_of(ph)) break;
-        total[ph] += pick(ph, (job_at(ph, job_i).count + 7) >> 3, (job_at(ph, job_i).count + 3) >> 2);
+      Items item;
+      for (begin_items(item, ph); there(item); next_item(item)) {
+        const int count = job_at(ph, item.job).count;
+        total[ph] += pick(ph, (count + 7) >> 3, (count + 3) >> 2);
       }
     }
     const int rounds = total[0] + total[1];
