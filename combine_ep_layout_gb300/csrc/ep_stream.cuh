@@ -73,13 +73,36 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // half word is already q * 2^-133, and one in bits 4-7 is 16 q * 2^-133: masks and
 // one shift make the operands of eight weights.  The activations carry the rest:
 // times 2^64, the odd columns (bits 4-7) times 2^60, exact in bf16 for magnitudes
-// below 2^64 (a larger one counts as infinite).  The offset of 8 is a product too:
+// below 2^64.  (A larger one becomes infinite and its offset as well, so the sum is
+// NaN: see plain_dot.)  The offset of 8 is a product too:
 // a row of -8 for every column, the same for all rows, added to each group's sums
 // before its scale.  (Making q - 8 by or-ing an exponent and subtracting took 11
 // instructions for the 5 here, on the pipe that bounds these kernels.)
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
 constexpr float kUnit = 590295810358705651712.0f;   // 2^69: what sums of such products are to be multiplied by
+
+// (L2's value: it may be another block's, written since this one began)
+__device__ __forceinline__ float load_bf16(const __nv_bfloat16* at) {
+  return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(at))) << 16);
+}
+// A row of 4-bit weights times x (+ x_lo where given), product by product: what a
+// value is that came out NaN above, be it from activations of 2^64 and more, from
+// infinite ones, whose products have each its own sign, or from a NaN.
+static __device__ __noinline__ float plain_dot(const uint8_t* q, const float* scales, const __nv_bfloat16* x,
+                                               const __nv_bfloat16* x_lo, int cols, int group) {
+  float sum = 0.0f;
+  for (int c0 = 0; c0 < cols && !(sum != sum); c0 += group) {
+    float part = 0.0f;
+    for (int c = c0; c < c0 + group; ++c) {
+      const int nibble = q[c / 2] >> (4 * (c & 1)) & 15;
+      const float v = load_bf16(x + c) + (x_lo ? load_bf16(x_lo + c) : 0.0f);
+      part = fmaf(static_cast<float>(nibble - 8), v, part);
+    }
+    sum = fmaf(scales[c0 / group], part, sum);
+  }
+  return sum;
+}
 
 // Two neighbouring activations (even and odd column) as operands.
 __device__ __forceinline__ uint32_t lift(uint32_t x) {

@@ -37,6 +37,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
 __device__ __forceinline__ void store(const W4Params& p, int token, int row, float v) {
+  if (v != v)
+    v = stream::plain_dot(p.q + static_cast<int64_t>(row) * (p.cols / 2), p.scales + static_cast<int64_t>(row) * (p.cols / p.group),
+                          static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(token) * p.cols, nullptr, p.cols, p.group);
   const int64_t o = static_cast<int64_t>(token) * p.rows + row;
   if (p.out_f32)
     static_cast<float*>(p.out)[o] = v;

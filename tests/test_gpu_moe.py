@@ -223,6 +223,31 @@ def test_masked_entries(weights, group):
     assert m.status() == 0
 
 
+@pytest.mark.parametrize("weights,group", [("bf16", 0), ("int4", 32), ("int4", 128)])
+@pytest.mark.parametrize("n", [2, 20])
+def test_huge_activations(n, weights, group):
+    # the columns that only the up projection reads, times 2^66: h and the output scale with them
+    E, H, I, K = 6, 256, 128, 2
+    m, wt = handle(E, H, I, K, weights, group), make(E, H, I, weights, group, exact=True)
+    x, idx, w = tokens(n, H, E, K, exact=True)
+    x[::2, 1:8] *= 2.0 ** 66
+    check(m, x, idx, w, wt, dtype=torch.float32, exact=True)
+
+
+@pytest.mark.parametrize("weights,group", FORMS)
+def test_infinite_activations_are_not_hidden(weights, group):
+    E, H, I, K, n = 4, 128, 64, 1, 5
+    m, wt = handle(E, H, I, K, weights, group), make(E, H, I, weights, group)
+    x, idx, w = tokens(n, H, E, K)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    m.forward(x, idx, w, wt, a)
+    bad = x.clone()
+    bad[2, 5] = float("inf")
+    m.forward(bad, idx, w, wt, b)
+    keep = [t for t in range(n) if t != 2]
+    assert torch.equal(a[keep], b[keep]) and not torch.isfinite(b[2]).any() and m.status() == 0
+
+
 def test_ids_out_of_range_are_skipped_and_reported():
     E, H, I, K, n = 5, 64, 64, 3, 6
     m, wt = handle(E, H, I, K), make(E, H, I)

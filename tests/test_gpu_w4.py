@@ -115,6 +115,22 @@ def test_a_token_of_nan_or_infinity_stays_its_own():
     assert got[7][w == 0].isnan().all() and torch.equal(got[7][w > 0], torch.full_like(got[7][w > 0], float("inf")))
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 11, 33, 64])
+def test_huge_activations_are_exact_and_infinite_ones_keep_their_sign(n):
+    # all of a token times 2^70; an infinite column in another token
+    x, q, s = make(n, 100, 512, 64, True)
+    big = x.clone()
+    big[n // 2] *= 2.0 ** 70
+    check(big, q, s, torch.float32, True)
+    big[0] = 0.0
+    big[0, 77] = -float("inf")
+    out = torch.empty((n, 100), device="cuda")
+    ep.ep_w4_linear(big, q, s, out)
+    w = dense(q, s)[:, 77]
+    assert out[0][w == 0].isnan().all()
+    assert (out[0][w > 0] == -float("inf")).all() and (out[0][w < 0] == float("inf")).all()
+
+
 def test_scales_of_zero_and_negative_scales():
     x, q, s = make(4, 64, 256, 64, True)
     s[::3] = 0.0
