@@ -67,17 +67,25 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Nibbles as bf16 operands without arithmetic.  The bf16 codes 0 to 255 are the
-// values code * 2^-133 (subnormals, and the first binade goes on at their spacing),
-// and the matrix instruction takes them as such.  So a nibble q in bits 0-3 of a
-// half word is already q * 2^-133, and one in bits 4-7 is 16 q * 2^-133: masks and
-// one shift make the operands of eight weights.  The activations carry the rest:
-// times 2^64, the odd columns (bits 4-7) times 2^60, exact in bf16 for magnitudes
-// below 2^64.  (A larger one becomes infinite and its offset as well, so the sum is
-// NaN: see plain_dot.)  The offset of 8 is a product too:
-// a row of -8 for every column, the same for all rows, added to each group's sums
-// before its scale.  (Making q - 8 by or-ing an exponent and subtracting took 11
-// instructions for the 5 here, on the pipe that bounds these kernels.)
+// Nibbles become bf16 operands in one of two ways.
+//
+// Lifted: the bf16 codes 0 to 255 are the values code * 2^-133 (subnormals, and the
+// first binade goes on at their spacing), and the matrix instruction takes them as
+// such.  So a nibble q in bits 0-3 of a half word is already q * 2^-133, and one in
+// bits 4-7 is 16 q * 2^-133: masks and one shift, 5 instructions, make the operands
+// of eight weights.  The activations carry the rest: times 2^64, the odd columns (bits
+// 4-7) times 2^60, exact in bf16 for magnitudes below 2^64.  (A larger one becomes
+// infinite and its offset as well, so the sum is NaN: see plain_dot.)  The offset of
+// 8 is a product too: a row of -8 for every column, the same for all rows, added to
+// each group's sums before its scale.  That is 4 instructions and a matrix
+// instruction for each 8 activations.
+//
+// Plain: or-ing an exponent makes the bf16 128 + q, subtracting 136 leaves q - 8: 11
+// instructions for eight weights, none for the activations.
+//
+// Lifted wins where few columns meet many rows (one column tile: 5 tokens over 128
+// experts of 4096 x 1408, 115 -> 106 us), plain where one row tile meets many
+// columns (32 tokens, 4096 x 14336: 30 -> 23 us).
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
 constexpr float kUnit = 590295810358705651712.0f;   // 2^69: what sums of such products are to be multiplied by
@@ -102,6 +110,15 @@ static __device__ __noinline__ float plain_dot(const uint8_t* q, const float* sc
     sum = fmaf(scales[c0 / group], part, sum);
   }
   return sum;
+}
+
+// Two of a word's nibbles (bits 0-3 and 16-19 of v) as bf16 values nibble - 8.
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t v) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(u) : "r"(v));
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   __nv_bfloat162(__float2bfloat16(136.0f), __float2bfloat16(136.0f)));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Two neighbouring activations (even and odd column) as operands.
@@ -146,9 +163,9 @@ struct Form {
   __device__ static __forceinline__ uint32_t x_offset(int col, int c) { return kABytes + kSBytes + x_at(col, c); }
 };
 
-// acc[rt][nt] += (in units of 2^-69 for 4-bit weights) tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
-// and scales at `slot`, columns at `cols`.
-template <int G, int RT, int NT, int CAP>
+// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage (lifted
+// 4-bit weights: in units of 1 / kUnit): weights and scales at `slot`, columns at `cols`.
+template <int G, int RT, int NT, int CAP, bool LIFT = true>
 __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* cols, int lane, float (&acc)[RT][CAP][4]) {
   using F = Form<G, RT>;
   const int g = lane >> 2, t = lane & 3;
@@ -176,7 +193,8 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
     // nibble i + 4, and the activations are paired the same way.
 #pragma unroll
     for (int grp = 0; grp < F::kScales; ++grp) {
-      float sum[F::kRowTiles][NT][4], offset[NT][4];
+      float sum[F::kRowTiles][NT][4];
+      [[maybe_unused]] float offset[NT][4];
 #pragma unroll
       for (int q = grp * (G / 32); q < (grp + 1) * (G / 32); ++q) {
         const bool first = q == grp * (G / 32);
@@ -184,29 +202,39 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
-          x.x = lift(x.x), x.y = lift(x.y), x.z = lift(x.z), x.w = lift(x.w);
+          if constexpr (LIFT) x.x = lift(x.x), x.y = lift(x.y), x.z = lift(x.z), x.w = lift(x.w);
           b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
           b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
           b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
           b[nt][3] = __byte_perm(x.y, x.w, 0x7632);
-          if (first)
-            mma_first(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
-          else
-            mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
-          mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][2], b[nt][3]);
+          if constexpr (LIFT) {
+            if (first)
+              mma_first(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
+            else
+              mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
+            mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][2], b[nt][3]);
+          }
         }
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
           const uint32_t lo = load4(slot + F::a_offset(16 * rt + g, q) + 4 * t);
           const uint32_t hi = load4(slot + F::a_offset(16 * rt + g + 8, q) + 4 * t);
-          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+          uint32_t a[8];
+          if constexpr (LIFT) {
+            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+            a[0] = lo & kLow, a[1] = hi & kLow, a[2] = lo & kHigh, a[3] = hi & kHigh;
+            a[4] = lo8 & kLow, a[5] = hi8 & kLow, a[6] = lo8 & kHigh, a[7] = hi8 & kHigh;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[2 * i] = nibble_pair(lo >> 4 * i), a[2 * i + 1] = nibble_pair(hi >> 4 * i);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             if (first)
-              mma_first(sum[rt][nt], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, b[nt][0], b[nt][1]);
+              mma_first(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
             else
-              mma(sum[rt][nt], lo & kLow, hi & kLow, lo & kHigh, hi & kHigh, b[nt][0], b[nt][1]);
-            mma(sum[rt][nt], lo8 & kLow, hi8 & kLow, lo8 & kHigh, hi8 & kHigh, b[nt][2], b[nt][3]);
+              mma(sum[rt][nt], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
+            mma(sum[rt][nt], a[4], a[5], a[6], a[7], b[nt][2], b[nt][3]);
           }
         }
       }
@@ -216,10 +244,10 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
         const float s1 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          acc[rt][nt][0] = fmaf(s0, sum[rt][nt][0] + offset[nt][0], acc[rt][nt][0]);
-          acc[rt][nt][1] = fmaf(s0, sum[rt][nt][1] + offset[nt][1], acc[rt][nt][1]);
-          acc[rt][nt][2] = fmaf(s1, sum[rt][nt][2] + offset[nt][2], acc[rt][nt][2]);
-          acc[rt][nt][3] = fmaf(s1, sum[rt][nt][3] + offset[nt][3], acc[rt][nt][3]);
+          acc[rt][nt][0] = fmaf(s0, LIFT ? sum[rt][nt][0] + offset[nt][0] : sum[rt][nt][0], acc[rt][nt][0]);
+          acc[rt][nt][1] = fmaf(s0, LIFT ? sum[rt][nt][1] + offset[nt][1] : sum[rt][nt][1], acc[rt][nt][1]);
+          acc[rt][nt][2] = fmaf(s1, LIFT ? sum[rt][nt][2] + offset[nt][2] : sum[rt][nt][2], acc[rt][nt][2]);
+          acc[rt][nt][3] = fmaf(s1, LIFT ? sum[rt][nt][3] + offset[nt][3] : sum[rt][nt][3], acc[rt][nt][3]);
         }
       }
     }
