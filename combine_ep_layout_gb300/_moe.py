@@ -177,22 +177,24 @@ class EpMoeWeights:
         _require(w13.dtype == w2.dtype == (torch.uint8 if q else torch.bfloat16),
                  "w13 and w2 must be bf16, or uint8 with scales")
         _require(not q or w13_scales.dtype == w2_scales.dtype == torch.float32, "scales must be fp32")
+        E, H = w2.shape[0], w2.shape[1]
+        I = w13.shape[1] // 2
+        per = 2 if q else 1
+        g = H // max(1, w13_scales.shape[2]) if q else 0
+        want = [(w13, (E, 2 * I, H // per)), (w2, (E, H, I // per))]
+        if q:
+            want += [(w13_scales, (E, 2 * I, H // max(g, 1))), (w2_scales, (E, H, I // max(g, 1)))]
+        for t, shape in want:
+            _require(tuple(t.shape) == shape, "weights have shape %s, expected %s" % (tuple(t.shape), shape))
         self.int4 = q
+        self.dims = (E, H, I, g)
         self.c = ep_moe_weights_t(w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(), _ptr(w2_scales))
-        self._fits = None
 
     def check(self, cfg):
-        """Raise unless the shapes are those of cfg (looked at once per configuration object)."""
-        if self._fits is cfg:
-            return
-        E, H, I, g = cfg.num_experts, cfg.hidden_dim, cfg.intermediate_dim, cfg.group_size
+        """Raise unless the weights are those of cfg."""
         _require(self.int4 == (cfg.weight_dtype == EP_INT4X2), "weights are not of the handle's weight_dtype")
-        per = 2 if self.int4 else 1
-        want = [(E, 2 * I, H // per), (E, H, I // per)]
-        want += [(E, 2 * I, H // g), (E, H, I // g)] if self.int4 else []
-        for t, s in zip(self.tensors, want):
-            _require(tuple(t.shape) == s, "weights have shape %s, expected %s" % (tuple(t.shape), s))
-        self._fits = cfg
+        _require(self.dims == (cfg.num_experts, cfg.hidden_dim, cfg.intermediate_dim, cfg.group_size),
+                 "weights are (experts, hidden, intermediate, group) %s, expected those of the handle" % (self.dims,))
 
 
 class EpMoe:
