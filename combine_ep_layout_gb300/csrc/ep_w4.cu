@@ -4,10 +4,11 @@
 // Bound by reading the weights once, as long as turning nibbles into operands
 // keeps up.  Two kernels, by the number of tokens:
 //
-//   narrow (up to 8 tokens)  a block of 8 warps takes 16 RT rows; its warps split
+//   narrow (up to 8 tokens)  a block of 8 warps takes 32 rows; its warps split
 //       the columns chunk by chunk, each through its own cp.async ring
-//       (ep_stream.cuh), and add their sums through shared memory.  Small tiles
-//       and many blocks: a few MB of weights have to reach every SM at once.
+//       (ep_stream.cuh), and add their sums through shared memory.  Small tiles,
+//       as a few MB of weights have to reach every SM at once; where there are more
+//       than fit, a block goes on to the next tile with its rings full.
 //   wide (9 to 64 tokens)    each of a block's 4 warps takes its own 16 rows and all
 //       share a stage's activations, which would outweigh the weights if every
 //       warp had its own.  Bound by the instructions that make operands of
@@ -94,50 +95,60 @@ __device__ __forceinline__ void put_sums(float* red, int row0, int lane, float u
 
 // ------------------------------------------------------------------ narrow
 
-template <int G, int RT>
+template <int G, int NT>
 struct Narrow {
-  using F = Form<G, RT>;
-  static constexpr int kStages = RT == 1 ? 6 : 4;
-  static constexpr int kWarpRed = 8 * (F::kRows + 4);            // floats of one warp's sums
+  static constexpr int kRowTiles = 2;
+  using F = Form<G, kRowTiles>;
+  static constexpr int kStages = NT == 1 ? 3 : 2;
+  static constexpr int kFit = 2;                                 // blocks that fit together
+  static constexpr int kWarpRed = 8 * NT * (F::kRows + 4);            // floats of one warp's sums
   static constexpr int kRed = kWarps * kWarpRed * 4;
   // the columns that no token fills are read (and not used) past the last slot
   static constexpr int slot(int n) { return F::kABytes + F::kSBytes + n * F::kXBytes; }
+  // (past the last one are the sums)
+  static constexpr int ring(int n) { return kWarps * kStages * slot(n); }
   static constexpr int bytes(int n) {
-    const int ring = kWarps * kStages * slot(n) + (8 - n) * F::kXBytes;
-    return ring > kRed ? ring : kRed;
+    const int over = (8 * NT - n) * F::kXBytes;
+    return ring(n) + (kRed > over ? kRed : over);
   }
 };
 
-template <int G, int RT>
-__global__ void __launch_bounds__(kThreads) w4_narrow_kernel(const W4Params p, int splits) {
-  using F = Form<G, RT>;
-  using S = Narrow<G, RT>;
-  constexpr int kStages = S::kStages;
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads, Narrow<G, NT>::kFit) w4_narrow_kernel(const W4Params p, int splits) {
+  using S = Narrow<G, NT>;
+  using F = typename S::F;
+  constexpr int kStages = S::kStages, RT = S::kRowTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tile = blockIdx.x / splits, part = blockIdx.x % splits;   // part: the rank in the cluster
+  const int part = blockIdx.x % splits;                               // the rank in the cluster
+  const int tiles = (p.rows + F::kRows - 1) / F::kRows, at_once = gridDim.x / splits;
   const int pieces = p.cols / 32, chunks = (p.cols + F::kCols - 1) / F::kCols;
   const int step = kWarps * splits, c0 = part * kWarps + warp;
   const bool whole = p.cols % 128 == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 15) == 0;
   const uint32_t slot_bytes = F::kABytes + F::kSBytes + p.n * F::kXBytes;
   const uint32_t ring = stream::smem_addr(smem) + warp * kStages * slot_bytes;
-  auto row_of = [&](int r) { return min(tile * F::kRows + r, p.rows - 1); };
+  // where the copies stand: chunk c of tile `ahead`
+  int ahead = blockIdx.x / splits, c = c0 < chunks ? c0 : chunks;
+  auto row_of = [&](int r) { return min(ahead * F::kRows + r, p.rows - 1); };
   const int lane_row = lane / F::kPieces, lane_piece = lane % F::kPieces;
-  const uint8_t* row_ptr[F::kCopies];
-#pragma unroll
-  for (int i = 0; i < F::kCopies; ++i)
-    row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane_row + i * (32 / F::kPieces))) * (p.cols / 2);
   const uint32_t a_dst = F::a_offset(lane_row, lane_piece);
-  constexpr int kScaleCopies = (F::kRows + 31) / 32, kXCopies = 8 * F::kXPieces / 32;
+  constexpr int kScaleCopies = (F::kRows + 31) / 32, kXCopies = 8 * NT * F::kXPieces / 32;
+  const uint8_t* row_ptr[F::kCopies];
   const float* s_src[kScaleCopies];
+  auto enter_tile = [&]() {
 #pragma unroll
-  for (int i = 0; i < kScaleCopies; ++i)
-    s_src[i] = p.scales + static_cast<int64_t>(row_of(lane + 32 * i)) * (p.cols / G);
+    for (int i = 0; i < F::kCopies; ++i)
+      row_ptr[i] = p.q + static_cast<int64_t>(row_of(lane_row + i * (32 / F::kPieces))) * (p.cols / 2);
+#pragma unroll
+    for (int i = 0; i < kScaleCopies; ++i)
+      s_src[i] = p.scales + static_cast<int64_t>(row_of(lane + 32 * i)) * (p.cols / G);
+  };
+  enter_tile();
   const int lane_col = lane / F::kXPieces, lane_xpiece = lane % F::kXPieces;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(lane_col) * p.cols;
-  auto issue = [&](int c, uint32_t slot) {
-    if (c < chunks) {
+  auto issue = [&](uint32_t slot) {
+    if (c < chunks && ahead < tiles) {
       const int piece = c * F::kPieces + lane_piece;
       const bool ok = piece < pieces;
       const int w_at = ok ? piece * 16 : 0;
@@ -161,41 +172,51 @@ __global__ void __launch_bounds__(kThreads) w4_narrow_kernel(const W4Params p, i
           stream::copy16(slot + F::x_offset(col, lane_xpiece),
                          x + static_cast<int64_t>(i * (32 / F::kXPieces)) * p.cols + x_at, at < p.cols);
       }
+      c += step;
+      if (c >= chunks) {
+        c = c0;
+        ahead += at_once;
+        if (ahead < tiles) enter_tile();
+      }
     }
     stream::commit();
   };
-  float acc[RT][1][4];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[rt][0][i] = 0.0f;
   grid_dependency_wait();   // nothing of memory has been touched before this
-  for (int s = 0; s < kStages - 1; ++s) issue(c0 + s * step, ring + s * slot_bytes);
   const uint32_t ring_bytes = kStages * slot_bytes;
+  for (int s = 0; s < kStages - 1; ++s) issue(ring + s * slot_bytes);
   uint32_t in = (kStages - 1) * slot_bytes, out = 0;
-  for (int c = c0; c < chunks; c += step) {
-    stream::wait<kStages - 2>();
-    __syncwarp();          // every lane's copies of this stage, and every lane done with the slot refilled next
-    issue(c + (kStages - 1) * step, ring + in);
-    in = in + slot_bytes == ring_bytes ? 0 : in + slot_bytes;
-    stream::consume<G, RT, 1, 1>(smem + warp * ring_bytes + out, lane, acc);
-    out = out + slot_bytes == ring_bytes ? 0 : out + slot_bytes;
+  float* red = reinterpret_cast<float*>(smem + kWarps * ring_bytes);
+  for (int tile = blockIdx.x / splits; tile < tiles; tile += at_once) {
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.0f;
+    for (int k = c0; k < chunks; k += step) {
+      stream::wait<kStages - 2>();
+      __syncwarp();        // every lane's copies of this stage, and every lane done with the slot refilled next
+      issue(ring + in);
+      in = in + slot_bytes == ring_bytes ? 0 : in + slot_bytes;
+      stream::consume<G, RT, NT, NT>(smem + warp * ring_bytes + out, lane, acc);
+      out = out + slot_bytes == ring_bytes ? 0 : out + slot_bytes;
+    }
+    put_sums<F::kRows>(red + warp * S::kWarpRed, 0, lane, stream::kUnit, acc);
+    __syncthreads();
+    // each thread adds the 8 warps' sums of its values and keeps them in the first
+    // warp's place, which nothing else reads
+    for (int v = tid; v < F::kRows * p.n; v += kThreads) {
+      float* at = red + sum_at<F::kRows>(v % F::kRows, v / F::kRows);
+      float sum = *at;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) sum += at[w * S::kWarpRed];
+      *at = sum;
+    }
+    finish<F::kRows, kThreads>(p, red, p.n, tile * F::kRows, part, splits);
+    if (splits == 1) __syncthreads();   // the next tile's sums take the same place
   }
   stream::wait<0>();
-  __syncthreads();         // the rings' memory now holds the sums
-  float* red = reinterpret_cast<float*>(smem);
-  put_sums<F::kRows>(red + warp * S::kWarpRed, 0, lane, stream::kUnit, acc);
-  __syncthreads();
-  // each thread adds the 8 warps' sums of its values and keeps them in the first
-  // warp's place, which nothing else reads
-  for (int v = tid; v < F::kRows * p.n; v += kThreads) {
-    float* at = red + sum_at<F::kRows>(v % F::kRows, v / F::kRows);
-    float sum = *at;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) sum += at[w * S::kWarpRed];
-    *at = sum;
-  }
-  finish<F::kRows, kThreads>(p, red, p.n, tile * F::kRows, part, splits);
 }
 
 // -------------------------------------------------------------------- wide
@@ -295,14 +316,15 @@ __global__ void __launch_bounds__(Wide<G, NT>::kThreads, Wide<G, NT>::kPerSm) w4
 
 // How many blocks of a cluster share a tile: the cheapest by the time of its stages,
 // one block's alone (`alone`, its latency) or all of an SM's blocks together
-// (`together` each), in units of 10 ns; a cluster's own cost is 1 us.  At most the
-// 8 blocks that a cluster may always have.
-int choose_splits(int tiles, int stages, int alone, int together) {
+// (`together` each), in units of 10 ns.  A block's beginning and end cost as much as
+// `ends` stages, a cluster 1 us more.  At most the 8 blocks that a cluster may always
+// have.
+int choose_splits(int tiles, int stages, int alone, int together, int ends) {
   int best = 1;
   int64_t least = INT64_MAX;
-  for (int s = 1; s <= 8; s *= 2) {
-    const int64_t each = (stages + s - 1) / s, per_sm = (static_cast<int64_t>(tiles) * s + 151) / 152;
-    int64_t cost = per_sm * each * together > each * alone ? per_sm * each * together : each * alone;
+  for (int s = 1; s <= 8 && s <= stages; s *= 2) {
+    const int64_t each = (stages + s - 1) / s + ends, per_sm = (static_cast<int64_t>(tiles) * s + 151) / 152;
+    int64_t cost = per_sm * together > alone ? per_sm * each * together : each * alone;
     if (s > 1) cost += 100;
     if (cost < least) least = cost, best = s;
   }
@@ -343,13 +365,16 @@ cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, in
   return cudaLaunchKernelEx(&cfg, kernel, p, splits);
 }
 
-template <int G, int RT>
+template <int G, int NT>
 cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
-  using S = Narrow<G, RT>;
+  using S = Narrow<G, NT>;
   static std::atomic<uint64_t> ready{0};
-  const int tiles = (p.rows + 16 * RT - 1) / (16 * RT), chunks = (p.cols + 127) / 128;
-  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 60, 20 * RT);
-  return launch(w4_narrow_kernel<G, RT>, ready, p, tiles, splits, kThreads, S::bytes(8), S::bytes(p.n), s);
+  const int tiles = (p.rows + S::F::kRows - 1) / S::F::kRows, chunks = (p.cols + 127) / 128;
+  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 60, 40, 3);
+  // as many tiles at once as the blocks that fit together can take
+  const int by_bytes = 228 * 1024 / (S::bytes(p.n) + 1024);
+  const int most = 152 * (by_bytes < S::kFit ? by_bytes : S::kFit) / splits;
+  return launch(w4_narrow_kernel<G, NT>, ready, p, tiles < most ? tiles : most, splits, kThreads, S::bytes(8 * NT), S::bytes(p.n), s);
 }
 
 template <int G, int NT>
@@ -357,17 +382,13 @@ cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
   using S = Wide<G, NT>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + S::kRows - 1) / S::kRows, chunks = (p.cols + 127) / 128;
-  return launch(w4_wide_kernel<G, NT>, ready, p, tiles, choose_splits(tiles, chunks, 90, 12 + 4 * NT), S::kThreads, S::kBytes,
+  return launch(w4_wide_kernel<G, NT>, ready, p, tiles, choose_splits(tiles, chunks, 90, 12 + 4 * NT, 4), S::kThreads, S::kBytes,
                 S::kBytes, s);
 }
 
 template <int G>
 cudaError_t launch_g(const W4Params& p, cudaStream_t s) {
-  // narrow: more rows a block with more tokens, so that the activations stay below
-  // half of what is read
-  if (p.n <= 2) return launch_narrow<G, 1>(p, s);
-  if (p.n <= 4) return launch_narrow<G, 2>(p, s);
-  if (p.n <= 8) return launch_narrow<G, 4>(p, s);
+  if (p.n <= 8) return launch_narrow<G, 1>(p, s);
   if (p.n <= 16) return launch_wide<G, 2>(p, s);
   if (p.n <= 32) return launch_wide<G, 4>(p, s);
   return launch_wide<G, 8>(p, s);
