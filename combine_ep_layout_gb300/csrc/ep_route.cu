@@ -254,6 +254,8 @@ __device__ __forceinline__ void store_row(T* row, int experts, int lane, bool ve
     if (j0 + v < experts) row[j0 + v] = from_float<T>(z[v]);
 }
 
+// The gradient where it reaches every expert (softmax, not renormalised): a warp a
+// token, as in the router.
 template <class T, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams p, bool vec, bool vec_out) {
   allow_dependent_grids();
@@ -264,46 +266,80 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteParams
   const T* row = static_cast<const T*>(p.logits) + t * p.row_stride;
   T* out = static_cast<T*>(p.grad) + t * p.grad_stride;
   int64_t id = -1;
-  float g = 0.0f, zk = -INFINITY;
+  float g = 0.0f, zk = -INFINITY, z[V];
   if (lane < p.topk) {
     id = p.idx_in[t * p.topk + lane];
     if (id < 0 || id >= p.experts) id = -1;
-    if (id >= 0) {
-      g = p.grad_w[t * p.topk + lane] * p.scale;
-      zk = fmaxf(as_float(row[id]), -INFINITY);
-    }
   }
-  const bool full = !p.sigmoid && !p.renorm;              // the gradient reaches every expert
-  float z[V], d;
-  if (full) {
-    load_row<T, V>(row, p.experts, lane, vec, z);
-    const float peak = warp_max(lane_max(z));
-    const float sum = exp_row(z, peak);
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const float fk = exp_below(zk, peak) * inv;
-    const float spread = warp_sum(id >= 0 ? g * fk : 0.0f);
-    d = fk * (g - spread);
-#pragma unroll
-    for (int v = 0; v < V; ++v) z[v] = z[v] > 0.0f ? -spread * z[v] * inv : 0.0f;
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) z[v] = 0.0f;
-    const float s = p.sigmoid ? sigmoid(zk) : 0.0f;
-    if (p.renorm) {
-      const float top = warp_max(zk);
-      float f = p.sigmoid ? sigmoid_scaled(zk, top) : exp_below(zk, top);
-      const float tot = warp_sum(f);
-      f = tot > 0.0f ? f / tot : 0.0f;
-      const float mean = warp_sum(id >= 0 ? g * f : 0.0f);
-      d = f * (g - mean);
-    } else {
-      d = s * g;
-    }
-    if (p.sigmoid) d *= 1.0f - s;
+  load_row<T, V>(row, p.experts, lane, vec, z);
+  if (id >= 0) {
+    g = p.grad_w[t * p.topk + lane] * p.scale;
+    zk = fmaxf(as_float(row[id]), -INFINITY);
   }
+  const float peak = warp_max(lane_max(z));
+  const float sum = exp_row(z, peak);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float fk = exp_below(zk, peak) * inv;
+  const float spread = warp_sum(id >= 0 ? g * fk : 0.0f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) z[v] = z[v] > 0.0f ? -spread * z[v] * inv : 0.0f;
   store_row<T, V>(out, p.experts, lane, vec_out, z);
   __syncwarp();                                           // the row's writes come before the K entries'
-  if (id >= 0) out[id] = from_float<T>(zk > -INFINITY ? d : 0.0f);
+  if (id >= 0) out[id] = from_float<T>(zk > -INFINITY ? fk * (g - spread) : 0.0f);
+}
+
+// The gradient where it stays with the chosen experts: GL (8 or 16, at least topk)
+// lanes a token, several tokens a warp; zeros for the rows, then the entries.
+template <class T, int GL>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_chosen_kernel(RouteParams p, bool vec_out) {
+  constexpr int kTokens = 32 / GL, kPer = 16 / sizeof(T);
+  allow_dependent_grids();
+  const int lane = threadIdx.x & 31, k = lane % GL;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+  const int64_t t = t0 + lane / GL;
+  grid_dependency_wait();
+  if (t0 >= p.n) return;
+  auto group_max = [](float v) {
+#pragma unroll
+    for (int d = GL / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  };
+  auto group_sum = [](float v) {
+#pragma unroll
+    for (int d = GL / 2; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+    return v;
+  };
+  int64_t id = -1;
+  float g = 0.0f, zk = -INFINITY;
+  if (t < p.n && k < p.topk) {
+    id = p.idx_in[t * p.topk + k];
+    if (id < 0 || id >= p.experts) id = -1;
+    if (id >= 0) {
+      g = p.grad_w[t * p.topk + k] * p.scale;
+      zk = fmaxf(as_float(static_cast<const T*>(p.logits)[t * p.row_stride + id]), -INFINITY);
+    }
+  }
+  for (int r = 0; r < kTokens && t0 + r < p.n; ++r) {
+    T* row = static_cast<T*>(p.grad) + (t0 + r) * p.grad_stride;
+    int j0 = 0;
+    if (vec_out) {
+      for (int j = lane * kPer; j + kPer <= p.experts; j += 32 * kPer) *reinterpret_cast<uint4*>(row + j) = make_uint4(0, 0, 0, 0);
+      j0 = p.experts / kPer * kPer;
+    }
+    for (int j = j0 + lane; j < p.experts; j += 32) row[j] = from_float<T>(0.0f);
+  }
+  const float s = p.sigmoid ? sigmoid(zk) : 0.0f;
+  float d = s * g;
+  if (p.renorm) {
+    const float top = group_max(zk);
+    float f = p.sigmoid ? sigmoid_scaled(zk, top) : exp_below(zk, top);
+    const float tot = group_sum(f);
+    f = tot > 0.0f ? f / tot : 0.0f;
+    d = f * (g - group_sum(id >= 0 ? g * f : 0.0f));
+  }
+  if (p.sigmoid) d *= 1.0f - s;
+  __syncwarp();                                           // the rows' writes come before the entries'
+  if (id >= 0) static_cast<T*>(p.grad)[t * p.grad_stride + id] = from_float<T>(zk > -INFINITY ? d : 0.0f);
 }
 
 bool aligned16(const void* p, int64_t stride_bytes) {
@@ -324,8 +360,14 @@ cudaError_t launch_v(const RouteParams& p, bool backward, cudaStream_t s) {
   static const bool pdl = PdlEnabled();
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (backward)
-    return cudaLaunchKernelEx(&cfg, route_backward_kernel<T, V>, p, vec, aligned16(p.grad, p.grad_stride * size));
+  if (backward) {
+    const bool vec_out = aligned16(p.grad, p.grad_stride * size);
+    if (!p.sigmoid && !p.renorm) return cudaLaunchKernelEx(&cfg, route_backward_kernel<T, V>, p, vec, vec_out);
+    const int tokens = p.topk <= 8 ? 4 : 2;
+    cfg.gridDim = dim3(static_cast<unsigned>((p.n + kWarps * tokens - 1) / (kWarps * tokens)));
+    return tokens == 4 ? cudaLaunchKernelEx(&cfg, route_backward_chosen_kernel<T, 8>, p, vec_out)
+                       : cudaLaunchKernelEx(&cfg, route_backward_chosen_kernel<T, 16>, p, vec_out);
+  }
   if (p.topk <= 8)
     return p.bias ? cudaLaunchKernelEx(&cfg, route_kernel<T, V, 8, true>, p, vec)
                   : cudaLaunchKernelEx(&cfg, route_kernel<T, V, 8, false>, p, vec);
