@@ -7,7 +7,7 @@
 // items: first the gate/up items (expert, 16 or more channels: the gate's and the up
 // projection's rows together, so that the product act(gate) up is formed where
 // the sums are), then the down items (expert, 32 or more output channels).  Eight
-// warps split an item's k range chunk by chunk; each streams its own chunks through
+// (4-bit: twelve) warps split an item's k range chunk by chunk; each streams its own chunks through
 // its own cp.async ring (ep_stream.cuh) across items and phases, so the ring never
 // drains.  For each column tile of an item (a round) they leave their sums in one
 // of two buffers and go on; two more warps, one for each buffer, add up the
@@ -30,6 +30,14 @@
 // same share, whichever was late (folded by the block that finished a tile last, 64
 // tokens' rows took the latest block 120 us).  No sum depends on the order of blocks:
 // equal inputs, equal bits.
+//
+// Measured with the router before it, of a copy's 6.8 TB/s: bf16, 64 experts of 7168 x
+// 2048, top-8: 1 token 116 us (6.1 TB/s), 8 tokens 537 us (6.9 TB/s), 64 tokens 0.94 ms
+// (6.0 TB/s: half the experts have more than the 8 tokens of a down job, so part of
+// w2 passes the SMs twice, at what L2 gives them).  4-bit, group 128, 128 experts of
+// 4096 x 1408, top-6: 8 tokens 104 us (3.6 TB/s), bound by instructions.  A layer of
+// 32 experts of 1024 x 512 takes 4 tokens 25 us: set-up 2.4, first weights 3.8, gate/up
+// 3.5, their fences 3, down 1.5, theirs and the fold 4.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -148,13 +156,16 @@ constexpr int lists_bytes(int entries) { return (entries * (4 + 4 + 2) + entries
 // HBM's full rate.
 template <int G, int NT>
 struct Shape {
-  // 4 row tiles spare 4-bit weights half the work on the activations; with 16
-  // columns they would leave the ring too short
+  // 4 row tiles spare 4-bit weights half the work on the activations (106 us, with 2
+  // 118 us: 8 tokens, 128 experts of 4096 x 1408); with 16 columns they would leave
+  // the ring too short
   static constexpr int kRowTiles = G != 0 && NT == 1 ? 4 : 2;
   // tokens of one job: gate/up a column each, down two columns each
   static constexpr int kCap0 = 8 * NT, kCap1 = 4 * NT;
   static constexpr int kEnough = 8, kItems = 4;              // stages of a warp in an item, items of a block (see widen)
   using F = Form<G, kRowTiles>;
+  // 4-bit weights take more instructions a byte: 12 warps (106 and 403 us for 8 and
+  // 64 tokens of those experts, with 8 warps 113 and 451 us)
   static constexpr int kWarps = G != 0 ? 12 : 8;
   static constexpr int kAllWarps = kWarps + kFinishers + 1;
   static constexpr int kThreads = 32 * kAllWarps;
@@ -303,8 +314,9 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   auto chunks = [&](int ph) { return pick(ph, chunks_0, chunks_1); };
   // An item is `wide` row tiles side by side, 1, 2 or 4, each with its share of the
   // warps: where the columns are few, one tile would give a warp so few stages that
-  // setting them up costs more than they do.  As long as every block keeps enough
-  // items for all to end together.
+  // setting them up costs more than they do (8 tokens, 128 4-bit experts of 4096 x
+  // 1408: 106 us, with one tile always 114; 64 tokens, 64 experts of 7168 x 2048: 0.94
+  // and 0.99 ms).  As long as every block keeps enough items for all to end together.
   auto widen = [&](int subtiles, int jobs, int n_chunks) {   // the logarithm of the tiles
     int r = 0;
     while (r < 2 && (n_chunks << r) < S::kEnough * kWarps && jobs * (((subtiles - 1) >> (r + 1)) + 1) >= S::kItems * grid) ++r;
@@ -800,9 +812,15 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT>, p);
 }
 
+// 4-bit weights with up to 8 tokens: one column tile and four row tiles a warp (8
+// tokens, 128 experts of 4096 x 1408: 106 us, with two and two 140 us).  For bf16 it
+// makes no difference (64 experts of 7168 x 2048, 1 token: 115.9 and 116.8 us; 8: 544
+// and 537 us), so there is one kernel.
 template <int G>
 cudaError_t launch_g(const MoeParams& p, int num_sms, cudaStream_t s) {
-  if (p.n <= 8) return launch<G, 1>(p, num_sms, s);
+  if constexpr (G != 0) {
+    if (p.n <= 8) return launch<G, 1>(p, num_sms, s);
+  }
   return launch<G, 2>(p, num_sms, s);
 }
 

