@@ -44,7 +44,6 @@
 #include <atomic>
 #include <cstdint>
 
-#include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
 #include "ep_stream.cuh"
 #include "ep_tma.cuh"
@@ -192,7 +191,6 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   __shared__ __align__(8) uint64_t s_free[2];
   __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
   __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
-  allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int entries = p.n * p.topk;
   float* red_all = reinterpret_cast<float*>(smem + S::kRing);
@@ -230,7 +228,6 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   const uint32_t free_bar = stream::smem_addr(s_free);
   for (int i = tid; i < p.experts * chunk_words; i += kThreads) by_chunk[i / chunk_words * 8 + i % chunk_words] = 0;
   __syncthreads();
-  grid_dependency_wait();   // no memory of the device has been touched before this
   for (int i0 = 32 * warp; i0 < entries; i0 += kThreads) {
     const int i = i0 + lane;
     int64_t id = -1;
@@ -801,14 +798,14 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeCooperative;   // every block resident: the waits on other blocks end
+  // Every block resident: the waits on other blocks end.  (Programmatic launch beside it
+  // was measured and changes nothing: the grid needs every SM's shared memory, so it
+  // starts when the one before it ends.)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  static const bool pdl = PdlEnabled();
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT>, p);
 }
 
