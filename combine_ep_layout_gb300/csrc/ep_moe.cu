@@ -45,6 +45,7 @@
 #include <cstdint>
 
 #include "ep_moe_kernels.hpp"
+#include "ep_route.cuh"
 #include "ep_stream.cuh"
 #include "ep_tma.cuh"
 #include "ep_types.cuh"
@@ -56,7 +57,7 @@ using stream::Form;
 
 constexpr int kFinishers = 2;             // warps that finish rounds, one buffer each
 constexpr int kMaxEntries = kFewTokens * 16;
-constexpr unsigned kAll = 0xffffffffu;
+using route::kAll;
 constexpr int kSmemLimit = 232448 - 3072;  // dynamic shared memory of one block (its static part aside)
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -176,7 +177,7 @@ struct Shape {
   static constexpr int kRing = kWarps * kStages * kSlot;
   static_assert(kStages >= 2);
   // the set-up's counts (of 2048 experts, 32 bytes and a word each) and ranks use the ring
-  static_assert(kRing >= 2048 * 36 + 4 * kMaxEntries);
+  static_assert(kRing >= 2048 * 36 + 4 * kMaxEntries + 2 * kOwnTokens * kOwnTopk + 4 * 32 * kOwnTokens);
 };
 
 template <int G, int NT>
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   constexpr int kThreads = S::kThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t scan_warp[kAllWarps];
+  __shared__ float own_weight[kOwnTokens * kOwnTopk];   // by entry, of tokens routed here
   __shared__ int s_flag, s_lost, s_rounds;
   __shared__ __align__(8) uint64_t s_free[2];
   __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
@@ -211,6 +213,8 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   int* first_of = reinterpret_cast<int*>(smem + 2048 * 32);               // by expert
   uint16_t* expert_of = reinterpret_cast<uint16_t*>(smem + 2048 * 36);    // by entry
   uint16_t* rank_of = expert_of + kMaxEntries;                            // within its chunk
+  int16_t* routed = reinterpret_cast<int16_t*>(rank_of + kMaxEntries);    // by entry: the expert, -1 for none
+  int* slots = reinterpret_cast<int*>(routed + kOwnTokens * kOwnTopk);    // 32 of each token
   const int chunk_words = (entries + 127) / 128;                          // of 4 bytes
   auto entries_before = [&](int e, int chunk) {
     int sum = 0;
@@ -227,11 +231,30 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   }
   const uint32_t free_bar = stream::smem_addr(s_free);
   for (int i = tid; i < p.experts * chunk_words; i += kThreads) by_chunk[i / chunk_words * 8 + i % chunk_words] = 0;
+  // a few tokens' routing, a warp each: every block for itself, the first one writes it down
+  if (p.logits && warp < p.n) {
+    const float* row = static_cast<const float*>(p.logits) + warp * p.logits_stride;
+    const __nv_bfloat16* row16 = static_cast<const __nv_bfloat16*>(p.logits) + warp * p.logits_stride;
+    auto score = [&](int j) { return fmaxf(p.logits_bf16 ? __bfloat162float(row16[j]) : row[j], -INFINITY); };
+    float key[kOwnExperts / 32];
+#pragma unroll
+    for (int v = 0; v < kOwnExperts / 32; ++v) key[v] = 32 * v + lane < p.experts ? score(32 * v + lane) : -INFINITY;
+    float zk = -INFINITY;
+    const int chosen = route::choose<kOwnExperts / 32, kOwnTopk, true>(key, p.topk, lane, slots + 32 * warp, score, zk);
+    const float f = route::chosen_weight(zk, p.sigmoid, p.renorm);
+    if (lane < p.topk) {
+      const int i = warp * p.topk + lane;
+      const float w = chosen >= 0 ? f * p.route_scale : 0.0f;
+      routed[i] = static_cast<int16_t>(chosen);
+      own_weight[i] = w;
+      if (blockIdx.x == 0) p.idx_out[i] = chosen, p.weights_out[i] = w;
+    }
+  }
   __syncthreads();
   for (int i0 = 32 * warp; i0 < entries; i0 += kThreads) {
     const int i = i0 + lane;
     int64_t id = -1;
-    if (i < entries) id = p.topk_idx[i];
+    if (i < entries) id = p.logits ? routed[i] : p.topk_idx[i];
     const bool ok = id >= 0 && id < p.experts;
     if (i < entries && !ok && id != -1 && blockIdx.x == 0) atomicOr(p.err, kErrBadExpert);
     const int e = ok ? static_cast<int>(id) : -1 - lane;
@@ -740,7 +763,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
           const int en = tok[i] * p.topk + k;
           if (c[i] < 0 || !(L.valid[en / 32] >> (en % 32) & 1)) continue;
           const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(en) * p.hidden + c[i]));
-          const float w = p.topk_weights[en];
+          const float w = p.logits ? own_weight[en] : p.topk_weights[en];
           sum[i].x = fmaf(w, y.x, sum[i].x), sum[i].y = fmaf(w, y.y, sum[i].y);
           sum[i].z = fmaf(w, y.z, sum[i].z), sum[i].w = fmaf(w, y.w, sum[i].w);
         }

@@ -337,7 +337,18 @@ int ep_moe_layer(ep_moe_t m, const ep_route_cfg_t* route, const void* x, int32_t
     if (route->num_experts != m->cfg.num_experts || route->topk != m->cfg.num_expert_per_token)
       return fail(EP_EINVAL, "the route cfg's num_experts and topk must be the handle's");
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (const cudaError_t e = LaunchRoute(r, s); e != cudaSuccess) return fail_cuda(e, "route launch");
+    if (RoutesItself(r)) {   // one launch for the whole layer
+      p.logits = r.logits;
+      p.logits_stride = r.row_stride;
+      p.idx_out = r.idx;
+      p.weights_out = r.weights;
+      p.route_scale = r.scale;
+      p.logits_bf16 = r.bf16;
+      p.sigmoid = r.sigmoid;
+      p.renorm = r.renorm;
+    } else if (const cudaError_t e = LaunchRoute(r, s); e != cudaSuccess) {
+      return fail_cuda(e, "route launch");
+    }
     return launch_moe(m, p, s);
   });
 }

@@ -45,6 +45,13 @@ struct MoeParams {
   const void* x;            // bf16 [n, H]
   const int64_t* topk_idx;  // [n, K]
   const float* topk_weights;
+  // not null: the kernel routes the tokens itself (RoutesItself) and writes idx_out and weights_out
+  const void* logits;       // [n, E], rows logits_stride elements apart
+  int64_t logits_stride;
+  int64_t* idx_out;         // [n, K]
+  float* weights_out;       // [n, K]
+  float route_scale;
+  bool logits_bf16, sigmoid, renorm;
   const void* w13;          // [E, 2I, H]
   const float* w13_scales;
   const void* w2;           // [E, H, I]
@@ -65,6 +72,13 @@ struct MoeParams {
   int32_t* err;
   uint64_t wait_ns;
 };
+
+// Whether the MoE kernel can take this routing over: a warp a token, few experts and
+// choices, weights that need no score but the chosen ones'.
+constexpr int kOwnTokens = 8, kOwnExperts = 256, kOwnTopk = 8;
+inline bool RoutesItself(const RouteParams& r) {
+  return r.n <= kOwnTokens && r.experts <= kOwnExperts && r.topk <= kOwnTopk && r.bias == nullptr && (r.renorm || r.sigmoid);
+}
 
 cudaError_t LaunchMoe(const MoeParams& p, int num_sms, cudaStream_t s);
 

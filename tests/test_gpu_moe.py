@@ -341,6 +341,37 @@ def test_layer_is_route_then_forward(weights, group):
     assert ((a.double() - ref).abs() <= tol + 2.0 ** -7.99 * ref.abs()).all()
 
 
+# the layer routes a few tokens in its own launch; whatever it does, it gives the router's bits
+LAYERS = [(1, 1, 1), (1, 64, 8), (8, 256, 8), (8, 250, 7), (3, 33, 2), (5, 8, 8), (2, 31, 5), (8, 128, 6),
+          (9, 64, 8), (8, 257, 4), (4, 40, 9), (8, 300, 16), (64, 256, 8), (33, 17, 3)]
+
+
+@pytest.mark.parametrize("n,E,K", LAYERS)
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("sigmoid", True), ("sigmoid", False), ("softmax", False)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_layer_gives_the_bits_of_route_and_forward(n, E, K, score, renorm, dtype):
+    H, I = 64, 32
+    m, wt = handle(E, H, I, K), make(E, H, I)
+    x, _, _ = tokens(n, H, E, K)
+    g = torch.Generator(device="cuda").manual_seed(n * 1000 + E)
+    wide = torch.randn((n, E + 3), device="cuda", generator=g)
+    wide[torch.rand((n, E + 3), device="cuda", generator=g) < 0.2] = float("-inf")
+    if n > 1:
+        wide[1] = float("-inf")                     # nothing left
+        wide[n - 1] = (2 * wide[n - 1]).round() / 2  # many equal scores
+    z = wide.to(dtype)[:, 2:2 + E]                  # strided, not 16-byte aligned
+    rc = ep.make_route_cfg(E, K, score, renorm, 1.5)
+    idx = torch.full((n, K), -9, dtype=torch.int64, device="cuda")
+    w = torch.full((n, K), float("nan"), device="cuda")
+    i2, w2 = torch.empty_like(idx), torch.empty_like(w)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    for bias in (None, torch.linspace(-0.1, 0.1, E, device="cuda")):
+        m.layer(rc, x, z, wt, idx, w, a, select_bias=bias)
+        ep.ep_route(rc, z, i2, w2, bias)
+        m.forward(x, i2, w2, wt, b)
+        assert torch.equal(idx, i2) and torch.equal(w, w2) and torch.equal(a, b) and m.status() == 0
+
+
 def test_agrees_with_layout_dispatch_experts_combine():
     # the same tokens through the framework's large-batch path, the experts in torch
     E, H, I, K, n = 32, 1024, 256, 4, 64
