@@ -15,6 +15,10 @@
 // one memory fence for all the rounds written since its last one.  So neither the
 // sums nor the microseconds of a fence and an atomic stop the streams.
 //
+// Up to 8 tokens are routed here as well, every block for itself, a warp a token (one
+// launch instead of two: 115.7 us for one token over 64 experts of 7168 x 2048, with
+// the router's own launch 116.9).
+//
 // A down item needs its expert's whole h: a counter per active expert, raised by
 // each finished gate/up item, is waited for (bounded) just before the item's
 // activations are copied; its weights are under way by then.  Experts come in one

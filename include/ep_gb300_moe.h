@@ -157,7 +157,10 @@ int ep_moe_forward(ep_moe_t m, const void *x, int32_t num_tokens, const int64_t 
 
 /* The whole layer: ep_route of logits [num_tokens, E] into topk_idx and
  * topk_weights (caller's buffers, as in ep_route), then ep_moe_forward with
- * them.  route->num_experts and route->topk must equal the handle's E and K. */
+ * them, to the same bits as those two calls.  route->num_experts and route->topk
+ * must equal the handle's E and K.  One launch where the layer's kernel routes the
+ * tokens itself (at most 8 tokens, 256 experts and 8 choices, no select_bias, and
+ * not the softmax without renormalisation), else two. */
 int ep_moe_layer(ep_moe_t m, const ep_route_cfg_t *route, const void *x, int32_t num_tokens,
                  const void *logits, int32_t logits_dtype, int64_t row_stride,
                  const float *select_bias, const ep_moe_weights_t *weights, const void *bias,
