@@ -836,15 +836,13 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT>, p);
 }
 
-// 4-bit weights with up to 8 tokens: one column tile and four row tiles a warp (8
-// tokens, 128 experts of 4096 x 1408: 106 us, with two and two 140 us).  For bf16 it
-// makes no difference (64 experts of 7168 x 2048, 1 token: 115.9 and 116.8 us; 8: 544
-// and 537 us), so there is one kernel.
+// One column tile a job for few tokens, which leaves the ring longer: for 4-bit weights
+// up to 8 tokens (128 experts of 4096 x 1408, 8 tokens: 106 us, with two tiles 140), for
+// bf16 up to the 4 that a down job then holds (64 experts of 7168 x 2048, 1 token: 112
+// us, with two tiles 114; 8 tokens: 537 and 527 us).
 template <int G>
 cudaError_t launch_g(const MoeParams& p, int num_sms, cudaStream_t s) {
-  if constexpr (G != 0) {
-    if (p.n <= 8) return launch<G, 1>(p, num_sms, s);
-  }
+  if (p.n <= (G != 0 ? 8 : 4)) return launch<G, 1>(p, num_sms, s);
   return launch<G, 2>(p, num_sms, s);
 }
 
