@@ -16,8 +16,8 @@
 // sums nor the microseconds of a fence and an atomic stop the streams.
 //
 // Up to 8 tokens are routed here as well, every block for itself, a warp a token (one
-// launch instead of two: 115.7 us for one token over 64 experts of 7168 x 2048, with
-// the router's own launch 116.9).
+// launch instead of two: one token over 64 experts of 7168 x 2048 takes 1.2 us less than
+// with the router's own launch).
 //
 // A down item needs its expert's whole h: a counter per active expert, raised by
 // each finished gate/up item, is waited for (bounded) just before the item's
@@ -36,11 +36,11 @@
 // equal inputs, equal bits.
 //
 // Measured with the router before it, of a copy's 6.8 TB/s: bf16, 64 experts of 7168 x
-// 2048, top-8: 1 token 116 us (6.1 TB/s), 8 tokens 537 us (6.9 TB/s), 64 tokens 0.94 ms
-// (6.0 TB/s: half the experts have more than the 8 tokens of a down job, so part of
+// 2048, top-8: 1 token 113 us (6.2 TB/s), 8 tokens 527 us (7.0 TB/s), 64 tokens 0.93 ms
+// (6.1 TB/s: half the experts have more than the 8 tokens of a down job, so part of
 // w2 passes the SMs twice, at what L2 gives them).  4-bit, group 128, 128 experts of
-// 4096 x 1408, top-6: 8 tokens 104 us (3.6 TB/s), bound by instructions.  A layer of
-// 32 experts of 1024 x 512 takes 4 tokens 25 us: set-up 2.4, first weights 3.8, gate/up
+// 4096 x 1408, top-6: 8 tokens 107 us (3.5 TB/s), bound by instructions.  A layer of
+// 32 experts of 1024 x 512 takes 4 tokens 24 us: set-up 2.4, first weights 3.8, gate/up
 // 3.5, their fences 3, down 1.5, theirs and the fold 4.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
