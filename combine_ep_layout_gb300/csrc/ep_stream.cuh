@@ -73,11 +73,12 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // first binade goes on at their spacing), and the matrix instruction takes them as
 // such.  So a nibble q in bits 0-3 of a half word is already q * 2^-133, and one in
 // bits 4-7 is 16 q * 2^-133: masks and one shift, 5 instructions, make the operands
-// of eight weights.  The activations carry the rest: times 2^64, the odd columns (bits
-// 4-7) times 2^60, exact in bf16 for magnitudes below 2^64.  (A larger one becomes
-// infinite and its offset as well, so the sum is NaN: see plain_dot.)  The offset of
-// 8 is a product too: a row of -8 for every column, the same for all rows, added to
-// each group's sums before its scale.  That is 4 instructions and a matrix
+// of eight weights.  The activations carry the rest: times 2^90, the odd columns (bits
+// 4-7) times 2^86, exact in bf16 for magnitudes below 2^38.  (A larger one becomes
+// infinite and its offset as well, so the sum is NaN: see plain_dot.)  The sums' last
+// bit is then worth 2^-149 2^43 = 2^-106: activations of 2^-80 lose nothing yet.  The
+// offset of 8 is a product too: a row of -8 for every column, the same for all rows,
+// added to each group's sums before its scale.  That is 4 instructions and a matrix
 // instruction for each 8 activations.
 //
 // Plain: or-ing an exponent makes the bf16 128 + q, subtracting 136 leaves q - 8: 11
@@ -88,14 +89,14 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // columns (32 tokens, 4096 x 14336: 30 -> 23 us).
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
-constexpr float kUnit = 590295810358705651712.0f;   // 2^69: what sums of such products are to be multiplied by
+constexpr float kUnit = 8796093022208.0f;   // 2^43: what sums of such products are to be multiplied by
 
 // (L2's value: it may be another block's, written since this one began)
 __device__ __forceinline__ float load_bf16(const __nv_bfloat16* at) {
   return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(at))) << 16);
 }
 // A row of 4-bit weights times x (+ x_lo where given), product by product: what a
-// value is that came out NaN above, be it from activations of 2^64 and more, from
+// value is that came out NaN above, be it from activations of 2^38 and more, from
 // infinite ones, whose products have each its own sign, or from a NaN.
 static __device__ __noinline__ float plain_dot(const uint8_t* q, const float* scales, const __nv_bfloat16* x,
                                                const __nv_bfloat16* x_lo, int cols, int group) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t v) {
 
 // Two neighbouring activations (even and odd column) as operands.
 __device__ __forceinline__ uint32_t lift(uint32_t x) {
-  const uint32_t by = 0x5d805f80u;                  // 2^60 (odd), 2^64 (even)
+  const uint32_t by = 0x6a806c80u;                  // 2^86 (odd), 2^90 (even)
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
   return r;

@@ -234,6 +234,17 @@ def test_huge_activations(n, weights, group):
     check(m, x, idx, w, wt, dtype=torch.float32, exact=True)
 
 
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("n", [2, 8, 20])
+def test_tiny_up_projection(n, group):
+    # its scales times 2^-80: h and the output scale with them
+    E, H, I, K = 6, 256, 128, 2
+    m, wt = handle(E, H, I, K, "int4", group), make(E, H, I, "int4", group, exact=True)
+    wt.tensors[2][:, I:] *= 2.0 ** -80
+    x, idx, w = tokens(n, H, E, K, exact=True)
+    check(m, x, idx, w, wt, dtype=torch.float32, exact=True)
+
+
 @pytest.mark.parametrize("weights,group", FORMS)
 def test_infinite_activations_are_not_hidden(weights, group):
     E, H, I, K, n = 4, 128, 64, 1, 5

@@ -131,6 +131,13 @@ def test_huge_activations_are_exact_and_infinite_ones_keep_their_sign(n):
     assert (out[0][w > 0] == -float("inf")).all() and (out[0][w < 0] == float("inf")).all()
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 11, 33, 64])
+def test_tiny_activations_are_exact(n):
+    x, q, s = make(n, 100, 512, 64, True)
+    x[::2] *= 2.0 ** -80
+    check(x, q, s, torch.float32, True)
+
+
 def test_scales_of_zero_and_negative_scales():
     x, q, s = make(4, 64, 256, 64, True)
     s[::3] = 0.0
