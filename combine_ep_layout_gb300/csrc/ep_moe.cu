@@ -39,7 +39,7 @@
 // 2048, top-8: 1 token 113 us (6.2 TB/s), 8 tokens 527 us (7.0 TB/s), 64 tokens 0.93 ms
 // (6.1 TB/s: half the experts have more than the 8 tokens of a down job, so part of
 // w2 passes the SMs twice, at what L2 gives them).  4-bit, group 128, 128 experts of
-// 4096 x 1408, top-6: 8 tokens 107 us (3.5 TB/s), bound by instructions.  A layer of
+// 4096 x 1408, top-6: 8 tokens 103-108 us (3.6 TB/s), bound by instructions.  A layer of
 // 32 experts of 1024 x 512 takes 4 tokens 24 us: set-up 2.4, first weights 3.8, gate/up
 // 3.5, their fences 3, down 1.5, theirs and the fold 4.
 #include <cuda_bf16.h>

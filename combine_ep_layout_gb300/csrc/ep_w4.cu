@@ -235,7 +235,10 @@ struct Wide {
   static constexpr int kXAt = kWarps * kWarpBytes;
   static constexpr int kSlot = kXAt + 8 * NT * F::kXBytes;
   static constexpr int kStages = 4;
-  static constexpr int kPerSm = NT == 8 ? 2 : 4;                 // blocks that fit together
+  // Blocks that fit together.  Up to 16 tokens 5: 20011 x 4096, 13 tokens, 21.4 us (4: 22.2,
+  // a few of its 626 blocks have to wait; 6: 27.0, too few registers); up to 32 tokens 4: 4096
+  // x 14336 23.4 us (5, with a stage less: 26.4); more: 2.
+  static constexpr int kPerSm = NT == 8 ? 2 : NT == 4 ? 4 : 5;
   static constexpr int kRows = kWarps * F::kRows;
   static constexpr int kRed = 8 * NT * (kRows + 4) * 4;
   static constexpr int kBytes = kStages * kSlot > kRed ? kStages * kSlot : kRed;
@@ -394,7 +397,7 @@ cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
 
 // Where narrow and wide meet: 4096 x 14336, 8 tokens 11.2 us narrow, 18.0 wide; 16
 // tokens (narrow with two column tiles) 17.6 and 18.4, but 20011 x 4096 with 13 tokens
-// 25.0 and 22.1.
+// 25.0 and 21.4.
 template <int G>
 cudaError_t launch_g(const W4Params& p, cudaStream_t s) {
   if (p.n <= 8) return launch_narrow<G, 1>(p, s);
