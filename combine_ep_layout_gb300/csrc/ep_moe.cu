@@ -82,18 +82,6 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-// Named barrier kBarFull + b: the streaming warps' sums of a round are in buffer b.
-// They arrive, the buffer's finishing warp waits.
-constexpr int kBarFull = 1;
-template <int THREADS>
-__device__ __forceinline__ void bar_arrive(int id) {
-  asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
-}
-template <int THREADS>
-__device__ __forceinline__ void bar_sync(int id) {
-  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
-}
-
 // Rounds written whose word to the other blocks may be outstanding; a power of two.
 constexpr int kQueue = 64;
 
@@ -103,32 +91,50 @@ constexpr int kQueue = 64;
 __device__ __forceinline__ int red_8(int row, int col) { return row * 8 + (col ^ (row >> 1 & 6)); }
 __device__ __forceinline__ int red_4(int row, int tok) { return row * 4 + (tok ^ (row >> 3 & 3)); }
 
-// Until the counter that other blocks raise is at `want`.  Gives up after wait_ns
-// (or at once where another wait of the block gave up): the launch goes on, in
-// bounds, and reports that its output is not valid.
+// Every wait is bounded.  Where one gives up, the block is lost: the launch's output is
+// not valid (the error word says so), the block's other waits give up as well, and each
+// warp stays away from what it waited for and leaves its phase.  No buffer is written
+// that may still be read, no word is told of a round that may not be written.
+__device__ __forceinline__ void lose(int* lost, int32_t* err) {
+  *static_cast<volatile int*>(lost) = 1;
+  atomicOr(err, kErrTimeout);
+}
+
+// Until the counter that other blocks raise is at `want`, for at most wait_ns.  The
+// caller goes on, in bounds.
 __device__ __forceinline__ void await_global(const int32_t* counter, int want, uint64_t wait_ns, int* lost, int32_t* err) {
   if (load_acquire(counter) >= want || *static_cast<volatile int*>(lost)) return;
   const uint64_t t0 = now_ns();
   while (load_acquire(counter) < want) {
     if (now_ns() - t0 > wait_ns) {
-      *static_cast<volatile int*>(lost) = 1;
-      atomicOr(err, kErrTimeout);
+      lose(lost, err);
       return;
     }
   }
 }
 
-// Until *count >= want, a count in shared memory that another warp raises; gives
-// up (false) after the clean-up limit.
-__device__ __forceinline__ bool await_count(const int* count, int want) {
-  const volatile int* c = count;
-  if (*c >= want) return true;
+// Waits of a whole warp on other warps of its block until test() holds, for at most limit_ns.
+// False, for every lane, where the block is lost.
+template <class Test>
+__device__ __forceinline__ bool await_block(Test test, uint64_t limit_ns, int* lost, int32_t* err) {
+  bool ok = test();
+  if (__all_sync(kAll, ok)) return true;
   const uint64_t t0 = now_ns();
-  while (*c < want) {
-    if (now_ns() - t0 > tma::kDrainNs) return false;
-    __nanosleep(64);
-  }
-  return true;
+  while (!ok && !*static_cast<volatile int*>(lost) && now_ns() - t0 < limit_ns) ok = test();
+  if (__all_sync(kAll, ok)) return true;
+  if ((threadIdx.x & 31) == 0) lose(lost, err);
+  return false;
+}
+// until the phase of a barrier with the given parity is over (the test may rest until it is,
+// but not with a limit of 0)
+__device__ __forceinline__ bool await_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, int* lost, int32_t* err) {
+  return await_block([&]() { return limit_ns ? tma::mbar_try_wait(bar, parity) : tma::mbar_test(bar, parity); }, limit_ns,
+                     lost, err);
+}
+// until *count >= want, a count in shared memory
+__device__ __forceinline__ bool await_count(const int* count, int want, uint64_t limit_ns, int* lost, int32_t* err) {
+  auto there = [&]() { return *static_cast<const volatile int*>(count) >= want; };
+  return __all_sync(kAll, there()) || await_block([&]() { __nanosleep(64); return there(); }, limit_ns, lost, err);
 }
 
 // A job: some tokens (at most the phase's cap, 16) of one active expert, in one
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   __shared__ uint64_t scan_warp[kAllWarps];
   __shared__ float own_weight[kOwnTokens * kOwnTopk];   // by entry, of tokens routed here
   __shared__ int s_flag, s_lost, s_rounds;
-  __shared__ __align__(8) uint64_t s_free[2];
+  __shared__ __align__(8) uint64_t s_full[2], s_free[2];   // by buffer: its sums are written, are read
   __shared__ int s_written[2], s_told;       // rounds written by each finisher, rounds told
   __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -231,9 +237,12 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   };
   if (tid == 0) {
     s_lost = s_rounds = s_written[0] = s_written[1] = s_told = 0;
-    for (int b = 0; b < 2; ++b) tma::mbar_init(stream::smem_addr(&s_free[b]), 1);
+    for (int b = 0; b < 2; ++b) {
+      tma::mbar_init(stream::smem_addr(&s_full[b]), kWarps);
+      tma::mbar_init(stream::smem_addr(&s_free[b]), 1);
+    }
   }
-  const uint32_t free_bar = stream::smem_addr(s_free);
+  const uint32_t full_bar = stream::smem_addr(s_full), free_bar = stream::smem_addr(s_free);
   for (int i = tid; i < p.experts * chunk_words; i += kThreads) by_chunk[i / chunk_words * 8 + i % chunk_words] = 0;
   // a few tokens' routing, a warp each: every block for itself, the first one writes it down
   if (p.logits && warp < p.n) {
@@ -547,9 +556,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   };
   int round = 0;
   int in = 0, out = 0;     // ring positions of the next stage to fill and to use
+  bool whole = true;       // no wait on the block gave up
   for (int s = 0; s < kStages - 1; ++s) issue(in), ++in;
 
-  for (phase = 0; phase < 2; ++phase) {
+  for (phase = 0; phase < 2 && whole; ++phase) {
     if (phase == 1 && ahead > 0) {
       Walk w;
       begin(w, 1);
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     }
     Items item;
     int c = lead(phase);
-    for (begin_items(item, phase); there(item); next_item(item)) {
+    for (begin_items(item, phase); whole && there(item); next_item(item)) {
       const Job job = job_at(phase, item.job);
       const int cols = phase == 0 ? job.count : 2 * job.count;
       const int nts = (cols + 7) >> 3;
@@ -603,8 +613,8 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
         if (nt >= nts) break;
         const int buf = round & 1;
         float* red = red_all + buf * (S::kRed / 4);
-        if (round >= 2 && !tma::mbar_wait_bounded(free_bar + 8 * buf, (round >> 1) - 1 & 1, tma::kDrainNs) && lane == 0)
-          atomicOr(p.err, kErrTimeout);
+        whole = round < 2 || await_phase(free_bar + 8 * buf, (round >> 1) - 1 & 1, p.block_wait_ns, &s_lost, p.err);
+        if (!whole) break;
         if (phase == 0) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
@@ -620,7 +630,8 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
             r0[red_4(16 * rt + g + 8, t)] = (acc[rt][nt][2] + acc[rt][nt][3]) * F::kOut;
           }
         }
-        bar_arrive<32 * (kWarps + 1)>(kBarFull + buf);
+        __syncwarp();
+        if (lane == 0) tma::mbar_arrive(full_bar + 8 * buf);
         ++round;
       }
     }
@@ -631,6 +642,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     const int buf = warp - kWarps;
     const float* red = red_all + buf * (S::kRed / 4);
     int round = 0;
+    bool whole = true;       // no wait on the block gave up
     auto plain_row = [&](int ph, int expert, int row, const __nv_bfloat16* x, const __nv_bfloat16* x_lo) {
       const int k = dim_k(ph);
       const int64_t at = static_cast<int64_t>(expert) * pick(ph, 2 * p.inter, p.hidden) + row;
@@ -651,13 +663,14 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     for (int phase = 0; phase < 2; ++phase) {
       const int step = kWarps >> pick(phase, side_0, side_1);
       Items item;
-      for (begin_items(item, phase); there(item); next_item(item)) {
+      for (begin_items(item, phase); whole && there(item); next_item(item)) {
         const Job job = job_at(phase, item.job);
         const int tile = item.tile;
         const int cols = pick(phase, 1, 2) * job.count;
         for (int nt = 0; 8 * nt < cols; ++nt, ++round) {
           if ((round & 1) != buf) continue;
-          bar_sync<32 * (kWarps + 1)>(kBarFull + buf);
+          whole = await_phase(full_bar + 8 * buf, round >> 1 & 1, p.block_wait_ns, &s_lost, p.err);
+          if (!whole) break;
           if (phase == 0) {
             const int n_cols = min(8, cols - 8 * nt);
             for (int v = lane; v < kHalf * n_cols << side_0; v += 32) {
@@ -703,9 +716,10 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
             }
           }
           __syncwarp();
+          if (lane == 0) tma::mbar_arrive(free_bar + 8 * buf);
+          whole = await_count(&s_told, round - kQueue + 1, p.block_wait_ns, &s_lost, p.err);
+          if (!whole) break;
           if (lane == 0) {
-            tma::mbar_arrive(free_bar + 8 * buf);
-            if (!await_count(&s_told, round - kQueue + 1)) atomicOr(p.err, kErrTimeout);
             queue[round % kQueue] = static_cast<uint16_t>(phase == 0 ? job.expert : tile);
             __threadfence_block();
             *static_cast<volatile int*>(&s_written[buf]) = (round >> 1) + 1;
@@ -725,8 +739,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     }
     const int rounds = total[0] + total[1];
     for (int told = 0; told < rounds;) {
-      if (!await_count(&s_written[told & 1], (told >> 1) + 1) && lane == 0) atomicOr(p.err, kErrTimeout);
-      __syncwarp();
+      if (!await_count(&s_written[told & 1], (told >> 1) + 1, p.block_wait_ns, &s_lost, p.err)) break;
       const int w0 = *static_cast<volatile int*>(&s_written[0]), w1 = *static_cast<volatile int*>(&s_written[1]);
       // even rounds below 2 w0 and odd rounds below 2 w1 are written
       const int upto = max(told + 1, min(min(2 * w0, 2 * w1 + 1), told + 32));

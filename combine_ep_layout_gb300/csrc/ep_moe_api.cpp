@@ -4,6 +4,7 @@
 // argument checked on the host before anything is launched.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -141,6 +142,9 @@ struct ep_moe {
 
 namespace {
 
+// What a block's warps may need of one another beside a wait for other blocks: microseconds.
+constexpr uint64_t kBlockWaitNs = 2000000000ull;
+
 // Checks of ep_moe_forward; fills the launch parameters.
 int check_forward(ep_moe_t m, const void* x, int32_t n, const int64_t* idx, const float* w,
                   const ep_moe_weights_t* wt, const void* bias, void* out, int32_t out_dtype, MoeParams* p) {
@@ -187,6 +191,9 @@ int check_forward(ep_moe_t m, const void* x, int32_t n, const int64_t* idx, cons
   p->blocks_done = m->blocks_done;
   p->err = m->err;
   p->wait_ns = m->wait_ns;
+  // A warp may wait for one that waits for another block, so that its limit has to be the
+  // longer one; 0 gives up at the first test everywhere.
+  p->block_wait_ns = m->wait_ns == 0 ? 0 : m->wait_ns + std::min(kBlockWaitNs, UINT64_MAX - m->wait_ns);
   return EP_OK;
 }
 

@@ -70,7 +70,8 @@ struct MoeParams {
   int32_t* tile_done;       // [H / 16] finished down rounds by channel tile
   int32_t* blocks_done;     // [1]
   int32_t* err;
-  uint64_t wait_ns;
+  uint64_t wait_ns;         // bound of one wait on other blocks
+  uint64_t block_wait_ns;   // bound of one wait on other warps of the block
 };
 
 // Whether the MoE kernel can take this routing over: a warp a token, few experts and
