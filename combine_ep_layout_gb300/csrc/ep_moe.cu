@@ -619,15 +619,15 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             float* r0 = red + warp * F::kRows * 8;
-            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g, 2 * t)) = make_float2(acc[rt][nt][0] * F::kOut, acc[rt][nt][1] * F::kOut);
-            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g + 8, 2 * t)) = make_float2(acc[rt][nt][2] * F::kOut, acc[rt][nt][3] * F::kOut);
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g, 2 * t)) = make_float2(acc[rt][nt][0], acc[rt][nt][1]);
+            *reinterpret_cast<float2*>(r0 + red_8(16 * rt + g + 8, 2 * t)) = make_float2(acc[rt][nt][2], acc[rt][nt][3]);
           }
         } else {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             float* r0 = red + warp * F::kRows * 4;
-            r0[red_4(16 * rt + g, t)] = (acc[rt][nt][0] + acc[rt][nt][1]) * F::kOut;
-            r0[red_4(16 * rt + g + 8, t)] = (acc[rt][nt][2] + acc[rt][nt][3]) * F::kOut;
+            r0[red_4(16 * rt + g, t)] = acc[rt][nt][0] + acc[rt][nt][1];
+            r0[red_4(16 * rt + g + 8, t)] = acc[rt][nt][2] + acc[rt][nt][3];
           }
         }
         __syncwarp();
@@ -643,12 +643,6 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     const float* red = red_all + buf * (S::kRed / 4);
     int round = 0;
     bool whole = true;       // no wait on the block gave up
-    auto plain_row = [&](int ph, int expert, int row, const __nv_bfloat16* x, const __nv_bfloat16* x_lo) {
-      const int k = dim_k(ph);
-      const int64_t at = static_cast<int64_t>(expert) * pick(ph, 2 * p.inter, p.hidden) + row;
-      return stream::plain_dot(static_cast<const uint8_t*>(pick(ph, p.w13, p.w2)) + at * (k / 2),
-                               pick(ph, p.w13_scales, p.w2_scales) + at * (k / p.group), x, x_lo, k, p.group);
-    };
     // the sums of the warps that share a row tile, in the order of warps
     auto add_up = [](const float* at, int stride, int warps) {
       float sum = 0.0f;
@@ -677,17 +671,9 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
               const int ch = v % kHalf, at = v / kHalf & ((1 << side_0) - 1), col = v / kHalf >> side_0;
               const int i = ((tile << side_0) + at) * kHalf + ch;
               const float* from = red + at * step * F::kRows * 8;
-              float gate = add_up(from + red_8(ch, col), F::kRows * 8, step);
-              float up = add_up(from + red_8(kHalf + ch, col), F::kRows * 8, step);
+              const float gate = add_up(from + red_8(ch, col), F::kRows * 8, step);
+              const float up = add_up(from + red_8(kHalf + ch, col), F::kRows * 8, step);
               if (i < p.inter) {
-                if constexpr (F::kInt4) {
-                  if (gate != gate || up != up) {
-                    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) +
-                                             static_cast<int64_t>(L.entry[job.start + 8 * nt + col] * by_topk >> 16) * p.hidden;
-                    gate = plain_row(0, job.expert, i, x, nullptr);
-                    up = plain_row(0, job.expert, p.inter + i, x, nullptr);
-                  }
-                }
                 const float h = activate(gate, p.act) * up;
                 const __nv_bfloat16 hi = __float2bfloat16_rn(h);
                 // an infinite or NaN h has nothing below it
@@ -704,14 +690,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
             for (int v = lane; v < F::kRows * n_tok << side_1; v += 32) {
               const int r = v % F::kRows, at = v / F::kRows & ((1 << side_1) - 1), tok = v / F::kRows >> side_1;
               const int c = ((tile << side_1) + at) * F::kRows + r;
-              float sum = add_up(red + at * step * F::kRows * 4 + red_4(r, tok), F::kRows * 4, step);
-              if constexpr (F::kInt4) {
-                if (c < p.hidden && sum != sum) {
-                  const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(p.h) +
-                                           2 * static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.inter;
-                  sum = plain_row(1, job.expert, c, h, h + p.inter);
-                }
-              }
+              const float sum = add_up(red + at * step * F::kRows * 4 + red_4(r, tok), F::kRows * 4, step);
               if (c < p.hidden) p.part[static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.hidden + c] = sum;
             }
           }

@@ -67,66 +67,24 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Nibbles become bf16 operands in one of two ways.
-//
-// Lifted: the bf16 codes 0 to 255 are the values code * 2^-133 (subnormals, and the
-// first binade goes on at their spacing), and the matrix instruction takes them as
-// such.  So a nibble q in bits 0-3 of a half word is already q * 2^-133, and one in
-// bits 4-7 is 16 q * 2^-133: masks and one shift, 5 instructions, make the operands
-// of eight weights.  The activations carry the rest: times 2^90, the odd columns (bits
-// 4-7) times 2^86, exact in bf16 for magnitudes below 2^38.  (A larger one becomes
-// infinite and its offset as well, so the sum is NaN: see plain_dot.)  The sums' last
-// bit is then worth 2^-149 2^43 = 2^-106: activations of 2^-80 lose nothing yet.  The
-// offset of 8 is a product too: a row of -8 for every column, the same for all rows,
-// added to each group's sums before its scale.  That is 4 instructions and a matrix
-// instruction for each 8 activations.
-//
-// Plain: or-ing an exponent makes the bf16 128 + q, subtracting 136 leaves q - 8: 11
-// instructions for eight weights, none for the activations.
-//
-// Lifted wins where few columns meet many rows (one column tile: 5 tokens over 128
-// experts of 4096 x 1408, 115 -> 106 us), plain where one row tile meets many
-// columns (32 tokens, 4096 x 14336: 30 -> 23 us).
+// Nibbles become bf16 operands by a mask and an fma.  The bf16 codes 0 to 255 are the
+// values code * 2^-133 (subnormals, and the first binade goes on at their spacing), so a
+// nibble q in bits 0-3 of a half word is q 2^-133 as it stands, and one in bits 4-7 is
+// 16 q 2^-133.  Times 2^127, or 2^123, less 2^-3, both are (q - 8) 2^-6, exactly: 9
+// instructions for eight weights (masks, one shift, four fma).  The unit goes into the
+// group's scale.  Every product with an activation is exact in fp32, subnormal activations
+// too, and infinite ones give what they give in fp32.  Or-ing an exponent and subtracting
+// 136 takes 11 instructions (7168 x 7168, 1 token: 9.8 us, this 9.3; 20011 x 4096, 13 tokens:
+// 20.6 and 20.0; MoE layer, 8 tokens, 128 experts of 4096 x 1408: 107 and 105).  Leaving q
+// in place and subtracting 8 times the sum of the activations afterwards takes 5, but the
+// two cancel: bits are lost wherever the activations share a sign.
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
-constexpr float kUnit = 8796093022208.0f;   // 2^43: what sums of such products are to be multiplied by
+constexpr uint32_t kLiftLow = 0x7f007f00u, kLiftHigh = 0x7d007d00u;   // 2^127, 2^123
+constexpr float kUnit = 64.0f;
 
-// (L2's value: it may be another block's, written since this one began)
-__device__ __forceinline__ float load_bf16(const __nv_bfloat16* at) {
-  return __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(at))) << 16);
-}
-// A row of 4-bit weights times x (+ x_lo where given), product by product: what a
-// value is that came out NaN above, be it from activations of 2^38 and more, from
-// infinite ones, whose products have each its own sign, or from a NaN.
-static __device__ __noinline__ float plain_dot(const uint8_t* q, const float* scales, const __nv_bfloat16* x,
-                                               const __nv_bfloat16* x_lo, int cols, int group) {
-  float sum = 0.0f;
-  for (int c0 = 0; c0 < cols && !(sum != sum); c0 += group) {
-    float part = 0.0f;
-    for (int c = c0; c < c0 + group; ++c) {
-      const int nibble = q[c / 2] >> (4 * (c & 1)) & 15;
-      const float v = load_bf16(x + c) + (x_lo ? load_bf16(x_lo + c) : 0.0f);
-      part = fmaf(static_cast<float>(nibble - 8), v, part);
-    }
-    sum = fmaf(scales[c0 / group], part, sum);
-  }
-  return sum;
-}
-
-// Two of a word's nibbles (bits 0-3 and 16-19 of v) as bf16 values nibble - 8.
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t v) {
-  uint32_t u;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(u) : "r"(v));
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                   __nv_bfloat162(__float2bfloat16(136.0f), __float2bfloat16(136.0f)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Two neighbouring activations (even and odd column) as operands.
-__device__ __forceinline__ uint32_t lift(uint32_t x) {
-  const uint32_t by = 0x6a806c80u;                  // 2^86 (odd), 2^90 (even)
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t masked, uint32_t lift) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(masked), "r"(lift), "r"(0xbe00be00u));   // -2^-3
   return r;
 }
 
@@ -149,8 +107,6 @@ struct Form {
 
   static constexpr int stage_bytes(int nt) { return kABytes + kSBytes + 8 * nt * kXBytes; }
 
-  static constexpr float kOut = kInt4 ? kUnit : 1.0f;     // what sums are to be multiplied by
-
   // Where piece c of weight row r lies in a stage: the 8 rows that a quarter
   // of the reading lanes touch fall on different banks.
   __device__ static __forceinline__ uint32_t a_offset(int r, int c) {
@@ -164,9 +120,9 @@ struct Form {
   __device__ static __forceinline__ uint32_t x_offset(int col, int c) { return kABytes + kSBytes + x_at(col, c); }
 };
 
-// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage (lifted
-// 4-bit weights: in units of 1 / kUnit): weights and scales at `slot`, columns at `cols`.
-template <int G, int RT, int NT, int CAP, bool LIFT = true>
+// acc[rt][nt] += tile rows (16 rt + ...) times columns (8 nt + ...) of a stage: weights
+// and scales at `slot`, columns at `cols`.
+template <int G, int RT, int NT, int CAP>
 __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* cols, int lane, float (&acc)[RT][CAP][4]) {
   using F = Form<G, RT>;
   const int g = lane >> 2, t = lane & 3;
@@ -195,39 +151,27 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
 #pragma unroll
     for (int grp = 0; grp < F::kScales; ++grp) {
       float sum[F::kRowTiles][NT][4];
-      [[maybe_unused]] float offset[NT][4];
 #pragma unroll
       for (int q = grp * (G / 32); q < (grp + 1) * (G / 32); ++q) {
         const bool first = q == grp * (G / 32);
         uint32_t b[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
-          if constexpr (LIFT) x.x = lift(x.x), x.y = lift(x.y), x.z = lift(x.z), x.w = lift(x.w);
+          const uint4 x = load16(cols + F::x_at(8 * nt + g, 4 * q + t));
           b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
           b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
           b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
           b[nt][3] = __byte_perm(x.y, x.w, 0x7632);
-          if constexpr (LIFT) {
-            if (first)
-              mma_first(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
-            else
-              mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][0], b[nt][1]);
-            mma(offset[nt], kMinus8, kMinus8, kMinus128, kMinus128, b[nt][2], b[nt][3]);
-          }
         }
 #pragma unroll
         for (int rt = 0; rt < F::kRowTiles; ++rt) {
           const uint32_t lo = load4(slot + F::a_offset(16 * rt + g, q) + 4 * t);
           const uint32_t hi = load4(slot + F::a_offset(16 * rt + g + 8, q) + 4 * t);
           uint32_t a[8];
-          if constexpr (LIFT) {
-            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-            a[0] = lo & kLow, a[1] = hi & kLow, a[2] = lo & kHigh, a[3] = hi & kHigh;
-            a[4] = lo8 & kLow, a[5] = hi8 & kLow, a[6] = lo8 & kHigh, a[7] = hi8 & kHigh;
-          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[2 * i] = nibble_pair(lo >> 4 * i), a[2 * i + 1] = nibble_pair(hi >> 4 * i);
+          for (int i = 0; i < 2; ++i) {
+            a[4 * i] = nibble_pair(lo >> 8 * i & kLow, kLiftLow), a[4 * i + 1] = nibble_pair(hi >> 8 * i & kLow, kLiftLow);
+            a[4 * i + 2] = nibble_pair(lo >> 8 * i & kHigh, kLiftHigh), a[4 * i + 3] = nibble_pair(hi >> 8 * i & kHigh, kLiftHigh);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -241,14 +185,14 @@ __device__ __forceinline__ void consume_at(const uint8_t* slot, const uint8_t* c
       }
 #pragma unroll
       for (int rt = 0; rt < F::kRowTiles; ++rt) {
-        const float s0 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g) * F::kScales + grp)));
-        const float s1 = __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp)));
+        const float s0 = kUnit * __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g) * F::kScales + grp)));
+        const float s1 = kUnit * __uint_as_float(load4(slot + F::kABytes + 4 * ((16 * rt + g + 8) * F::kScales + grp)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          acc[rt][nt][0] = fmaf(s0, LIFT ? sum[rt][nt][0] + offset[nt][0] : sum[rt][nt][0], acc[rt][nt][0]);
-          acc[rt][nt][1] = fmaf(s0, LIFT ? sum[rt][nt][1] + offset[nt][1] : sum[rt][nt][1], acc[rt][nt][1]);
-          acc[rt][nt][2] = fmaf(s1, LIFT ? sum[rt][nt][2] + offset[nt][2] : sum[rt][nt][2], acc[rt][nt][2]);
-          acc[rt][nt][3] = fmaf(s1, LIFT ? sum[rt][nt][3] + offset[nt][3] : sum[rt][nt][3], acc[rt][nt][3]);
+          acc[rt][nt][0] = fmaf(s0, sum[rt][nt][0], acc[rt][nt][0]);
+          acc[rt][nt][1] = fmaf(s0, sum[rt][nt][1], acc[rt][nt][1]);
+          acc[rt][nt][2] = fmaf(s1, sum[rt][nt][2], acc[rt][nt][2]);
+          acc[rt][nt][3] = fmaf(s1, sum[rt][nt][3], acc[rt][nt][3]);
         }
       }
     }

@@ -44,9 +44,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
 __device__ __forceinline__ void store(const W4Params& p, int token, int row, float v) {
-  if (v != v)
-    v = stream::plain_dot(p.q + static_cast<int64_t>(row) * (p.cols / 2), p.scales + static_cast<int64_t>(row) * (p.cols / p.group),
-                          static_cast<const __nv_bfloat16*>(p.x) + static_cast<int64_t>(token) * p.cols, nullptr, p.cols, p.group);
   const int64_t o = static_cast<int64_t>(token) * p.rows + row;
   if (p.out_f32)
     static_cast<float*>(p.out)[o] = v;
@@ -88,7 +85,7 @@ __device__ __forceinline__ void finish(const W4Params& p, float* red, int cols, 
 
 // A warp's fragments into such a tile.
 template <int ROWS, int RT, int NT>
-__device__ __forceinline__ void put_sums(float* red, int row0, int lane, float unit, const float (&acc)[RT][NT][4]) {
+__device__ __forceinline__ void put_sums(float* red, int row0, int lane, const float (&acc)[RT][NT][4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
@@ -96,7 +93,7 @@ __device__ __forceinline__ void put_sums(float* red, int row0, int lane, float u
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        red[sum_at<ROWS>(row0 + 16 * rt + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1))] = acc[rt][nt][i] * unit;
+        red[sum_at<ROWS>(row0 + 16 * rt + g + 8 * (i >> 1), 8 * nt + 2 * t + (i & 1))] = acc[rt][nt][i];
 }
 
 // ------------------------------------------------------------------ narrow
@@ -208,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, Narrow<G, NT>::kFit) w4_narrow_kerne
       stream::consume<G, RT, NT, NT>(smem + warp * ring_bytes + out, lane, acc);
       out = out + slot_bytes == ring_bytes ? 0 : out + slot_bytes;
     }
-    put_sums<F::kRows>(red + warp * S::kWarpRed, 0, lane, stream::kUnit, acc);
+    put_sums<F::kRows>(red + warp * S::kWarpRed, 0, lane, acc);
     __syncthreads();
     // each thread adds the 8 warps' sums of its values and keeps them in the first
     // warp's place, which nothing else reads
@@ -311,13 +308,13 @@ __global__ void __launch_bounds__(Wide<G, NT>::kThreads, Wide<G, NT>::kPerSm) w4
     issue(c + (kStages - 1) * splits, base + in * S::kSlot);
     in = in + 1 == kStages ? 0 : in + 1;
     const uint8_t* slot = smem + out * S::kSlot;
-    stream::consume_at<G, RT, NT, NT, false>(slot + warp * S::kWarpBytes, slot + S::kXAt, lane, acc);
+    stream::consume_at<G, RT, NT, NT>(slot + warp * S::kWarpBytes, slot + S::kXAt, lane, acc);
     out = out + 1 == kStages ? 0 : out + 1;
   }
   stream::wait<0>();
   __syncthreads();         // the ring's memory now holds the sums
   float* red = reinterpret_cast<float*>(smem);
-  put_sums<S::kRows>(red, warp * F::kRows, lane, 1.0f, acc);
+  put_sums<S::kRows>(red, warp * F::kRows, lane, acc);
   finish<S::kRows, S::kThreads>(p, red, p.n, tile * S::kRows, part, splits);
 }
 

@@ -80,14 +80,14 @@ int ep_route_backward(const ep_route_cfg_t *cfg, const void *logits, int32_t log
  *            and column 2b+1 in its high nibble
  *   scales   fp32 [rows, cols/group_size]
  *   W[r][c] = (nibble - 8) * scales[r][c / group_size]
- * group_size is 32, 64 or 128 and divides cols. */
+ * group_size is 32, 64 or 128 and divides cols; scales are below 2^122 in magnitude. */
 
 /* Largest num_tokens of ep_w4_linear and largest max_tokens of ep_moe_create. */
 #define EP_FEW_TOKENS 64
 
 /* out[t][r] = sum_c W[r][c] * x[t][c].  x: device bf16 [num_tokens, cols];
  * out: device bf16 or fp32 (out_dtype) [num_tokens, rows].  Products of bf16
- * x and the whole nibble values are summed in fp32 per group, the groups'
+ * x and nibble - 8, each exact, are summed in fp32 per group, the groups'
  * sums times their scales in fp32; one rounding to bf16 at the end.
  * 0 <= num_tokens <= EP_FEW_TOKENS, 1 <= rows <= 2^24, 1 <= cols <= 2^18; x and
  * qweight 16-byte aligned, scales and out aligned to their elements. */
