@@ -24,9 +24,12 @@
 // activations are copied; its weights are under way by then.  Experts come in one
 // order in both phases, so the wait is short unless few experts are active.
 //
-// h is kept as two bf16, h = hi + lo (16 significant bits), in two columns of the
-// down product whose sums are added: a column costs nothing until 4 tokens meet
-// on an expert, and the rounding of h to 8 bits would double the output's error.
+// h is kept as several bf16 that add up to it, in as many columns of the down product,
+// whose sums are added: two (16 significant bits) for a bf16 output, whose error would
+// double with one (columns cost nothing until 4 tokens meet on an expert); three (24 bits,
+// all of fp32's) for an fp32 output (2048 x 1024: off by 6e-7 of its norm, 2.4e-6 with two).
+// The three take four columns, so that a tile of 8 holds two tokens: 64 experts of 7168 x
+// 2048 take 1, 8 and 64 tokens 115, 542 and 1304 us, with a bf16 output 113, 527 and 921.
 //
 // The down items write fp32 expert rows.  A block that is through with its items
 // waits for the rounds of its share of the channel tiles and folds the K rows of
@@ -170,8 +173,8 @@ struct Shape {
   // 118 us: 8 tokens, 128 experts of 4096 x 1408); with 16 columns they would leave
   // the ring too short
   static constexpr int kRowTiles = G != 0 && NT == 1 ? 4 : 2;
-  // tokens of one job: gate/up a column each, down two columns each
-  static constexpr int kCap0 = 8 * NT, kCap1 = 4 * NT;
+  // columns of one job: gate/up a token each, down as many for a token as it has parts
+  static constexpr int kLogCap = NT == 1 ? 3 : 4, kCap = 1 << kLogCap;
   static constexpr int kEnough = 8, kItems = 4;              // stages of a warp in an item, items of a block (see widen)
   using F = Form<G, kRowTiles>;
   // 4-bit weights take more instructions a byte: 12 warps (106 and 403 us for 8 and
@@ -190,7 +193,8 @@ struct Shape {
   static_assert(kRing >= 2048 * 36 + 4 * kMaxEntries + 2 * kOwnTokens * kOwnTopk + 4 * 32 * kOwnTokens);
 };
 
-template <int G, int NT>
+// F32: fp32 output.
+template <int G, int NT, bool F32>
 __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const MoeParams p) {
   using S = Shape<G, NT>;
   using F = typename S::F;
@@ -205,6 +209,9 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   __shared__ uint16_t queue[kQueue];         // by round: the expert (gate/up) or the tile (down)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int entries = p.n * p.topk;
+  constexpr int h_rows = F32 ? 3 : 2;        // bf16 parts of h, rows of I next to one another
+  constexpr int log_part = F32 ? 2 : 1;      // columns of a token in the down product: 4 or 2
+  constexpr int log_toks = 3 - log_part;     // tokens of a column tile there: 2 or 4
   float* red_all = reinterpret_cast<float*>(smem + S::kRing);
   Lists L;
   {
@@ -286,17 +293,17 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     // three 16-bit sums in one word: entries, gate/up jobs, down jobs
     const int per = (p.experts + kThreads - 1) / kThreads, e0 = tid * per;
     const int e1 = min(e0 + per, p.experts);
-    auto word = [](int c) -> uint64_t {
+    auto word = [&](int c) -> uint64_t {
       return c == 0 ? 0
-                    : static_cast<uint64_t>(c) | static_cast<uint64_t>((c + S::kCap0 - 1) / S::kCap0) << 16 |
-                          static_cast<uint64_t>((c + S::kCap1 - 1) / S::kCap1) << 32;
+                    : static_cast<uint64_t>(c) | static_cast<uint64_t>((c - 1 >> S::kLogCap) + 1) << 16 |
+                          static_cast<uint64_t>((c - 1 >> (S::kLogCap - log_part)) + 1) << 32;
     };
     uint64_t mine = 0;
     int rounds = 0;        // down rounds of one channel tile
     for (int e = e0; e < e1; ++e) {
       const int c = entries_before(e, 4 * chunk_words);
       first_of[e] = c;
-      mine += word(c), rounds += (c + 3) >> 2;
+      mine += word(c), rounds += (c - 1 >> log_toks) + 1;   // (0 for c = 0)
     }
     if (rounds) atomicAdd(&s_rounds, rounds);
     uint64_t upto = mine;
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       if (c == 0) continue;
       const int start = static_cast<int>(base & 0xffff);
       for (int ph = 0; ph < 2; ++ph) {
-        const int cap = ph == 0 ? S::kCap0 : S::kCap1;
+        const int cap = ph == 0 ? S::kCap : S::kCap >> log_part;
         int j = static_cast<int>(base >> (16 + 16 * ph) & 0xffff);
         for (int o = 0; o < c; o += cap, ++j)
           (ph == 0 ? L.jobs_0 : L.jobs_1)[j] = pack_job(e, start + o, min(cap, c - o), (c + 7) >> 3);
@@ -349,10 +356,14 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   // warps: where the columns are few, one tile would give a warp so few stages that
   // setting them up costs more than they do (8 tokens, 128 4-bit experts of 4096 x
   // 1408: 106 us, with one tile always 114; 64 tokens, 64 experts of 7168 x 2048: 0.94
-  // and 0.99 ms).  As long as every block keeps enough items for all to end together.
+  // and 0.99 ms).  As long as every block keeps enough items for all to end together, and
+  // not for bf16 weights with an fp32 output: a warp's sums are then up to four times as
+  // long, and the matrix instruction's additions round worse than fp32's (2048 x 1024, 64
+  // tokens: off by 1.5e-6 of the output's norm, with one tile always 6.1e-7; 4-bit groups
+  // have sums of their own, 1.5e-7).
   auto widen = [&](int subtiles, int jobs, int n_chunks) {   // the logarithm of the tiles
     int r = 0;
-    while (r < 2 && (n_chunks << r) < S::kEnough * kWarps && jobs * (((subtiles - 1) >> (r + 1)) + 1) >= S::kItems * grid) ++r;
+    while (r < 2 && !(F32 && G == 0) && (n_chunks << r) < S::kEnough * kWarps && jobs * (((subtiles - 1) >> (r + 1)) + 1) >= S::kItems * grid) ++r;
     return r;
   };
   const int sub_0 = (p.inter + kHalf - 1) / kHalf, sub_1 = (p.hidden + F::kRows - 1) / F::kRows;
@@ -499,17 +510,20 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       }
     }
   };
-  // the activations' part: the job's columns (phase 1: the hi and the lo row of each entry)
+  // the activations' part: the job's columns (phase 1: the parts of each entry's h; what
+  // the fourth column of a token with three parts holds is not used)
   uint32_t x_off[kXCopies];                 // elements, from x or h
   int x_cols = 0;
   auto enter_columns = [&](const Walk& w) {
     const Job job = job_at(w.ph, w.job);
-    x_cols = pick(w.ph, 1, 2) * job.count;
+    x_cols = job.count << pick(w.ph, 0, log_part);
 #pragma unroll
     for (int i = 0; i < kXCopies; ++i) {
       const int col = lane_col + i * (32 / F::kXPieces);
       if (col < x_cols)
-        x_off[i] = (w.ph == 0 ? (L.entry[job.start + col] * by_topk >> 16) : 2u * L.entry[job.start + (col >> 1)] + static_cast<uint32_t>(col & 1)) *
+        x_off[i] = (w.ph == 0 ? (L.entry[job.start + col] * by_topk >> 16)
+                              : static_cast<uint32_t>(h_rows * L.entry[job.start + (col >> log_part)] +
+                                                      min(col & ((1 << log_part) - 1), h_rows - 1))) *
                    static_cast<uint32_t>(dim_k(w.ph));
     }
   };
@@ -584,7 +598,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
     int c = lead(phase);
     for (begin_items(item, phase); whole && there(item); next_item(item)) {
       const Job job = job_at(phase, item.job);
-      const int cols = phase == 0 ? job.count : 2 * job.count;
+      const int cols = job.count << (phase == 0 ? 0 : log_part);
       const int nts = (cols + 7) >> 3;
       float acc[RT][NT][4];
 #pragma unroll
@@ -626,8 +640,13 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             float* r0 = red + warp * F::kRows * 4;
-            r0[red_4(16 * rt + g, t)] = acc[rt][nt][0] + acc[rt][nt][1];
-            r0[red_4(16 * rt + g + 8, t)] = acc[rt][nt][2] + acc[rt][nt][3];
+            float lo = acc[rt][nt][0], hi = acc[rt][nt][2];
+            if (log_part == 1 || (t & 1) == 0) lo += acc[rt][nt][1], hi += acc[rt][nt][3];
+            if (log_part == 2) lo += __shfl_xor_sync(kAll, lo, 1), hi += __shfl_xor_sync(kAll, hi, 1);
+            if (log_part == 1 || (t & 1) == 0) {
+              r0[red_4(16 * rt + g, t >> (log_part - 1))] = lo;
+              r0[red_4(16 * rt + g + 8, t >> (log_part - 1))] = hi;
+            }
           }
         }
         __syncwarp();
@@ -660,7 +679,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       for (begin_items(item, phase); whole && there(item); next_item(item)) {
         const Job job = job_at(phase, item.job);
         const int tile = item.tile;
-        const int cols = pick(phase, 1, 2) * job.count;
+        const int cols = job.count << pick(phase, 0, log_part);
         for (int nt = 0; 8 * nt < cols; ++nt, ++round) {
           if ((round & 1) != buf) continue;
           whole = await_phase(full_bar + 8 * buf, round >> 1 & 1, p.block_wait_ns, &s_lost, p.err);
@@ -677,21 +696,22 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
                 const float h = activate(gate, p.act) * up;
                 const __nv_bfloat16 hi = __float2bfloat16_rn(h);
                 // an infinite or NaN h has nothing below it
-                const float rest = h - __bfloat162float(hi);
-                const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+                const float rest = fabsf(h - __bfloat162float(hi)) < INFINITY ? h - __bfloat162float(hi) : 0.0f;
+                const __nv_bfloat16 mid = __float2bfloat16_rn(rest);
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.h) +
-                                     2 * static_cast<int64_t>(L.entry[job.start + 8 * nt + col]) * p.inter + i;
+                                     static_cast<int64_t>(h_rows * L.entry[job.start + 8 * nt + col]) * p.inter + i;
                 dst[0] = hi;
-                dst[p.inter] = lo;
+                dst[p.inter] = mid;
+                if (h_rows == 3) dst[2 * p.inter] = __float2bfloat16_rn(rest - __bfloat162float(mid));
               }
             }
           } else {
-            const int n_tok = min(4, job.count - 4 * nt);
+            const int n_tok = min(1 << log_toks, job.count - (nt << log_toks));
             for (int v = lane; v < F::kRows * n_tok << side_1; v += 32) {
               const int r = v % F::kRows, at = v / F::kRows & ((1 << side_1) - 1), tok = v / F::kRows >> side_1;
               const int c = ((tile << side_1) + at) * F::kRows + r;
               const float sum = add_up(red + at * step * F::kRows * 4 + red_4(r, tok), F::kRows * 4, step);
-              if (c < p.hidden) p.part[static_cast<int64_t>(L.entry[job.start + 4 * nt + tok]) * p.hidden + c] = sum;
+              if (c < p.hidden) p.part[static_cast<int64_t>(L.entry[job.start + (nt << log_toks) + tok]) * p.hidden + c] = sum;
             }
           }
           __syncwarp();
@@ -713,7 +733,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
       Items item;
       for (begin_items(item, ph); there(item); next_item(item)) {
         const int count = job_at(ph, item.job).count;
-        total[ph] += pick(ph, (count + 7) >> 3, (count + 3) >> 2);
+        total[ph] += (count - 1 >> pick(ph, 3, log_toks)) + 1;
       }
     }
     const int rounds = total[0] + total[1];
@@ -773,7 +793,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
           sum[i].x += __uint_as_float(b.x << 16), sum[i].y += __uint_as_float(b.x & 0xffff0000u);
           sum[i].z += __uint_as_float(b.y << 16), sum[i].w += __uint_as_float(b.y & 0xffff0000u);
         }
-        if (p.out_f32) {
+        if constexpr (F32) {
           *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = sum[i];
         } else {
           const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[i].x, sum[i].y), hi = __floats2bfloat162_rn(sum[i].z, sum[i].w);
@@ -798,7 +818,7 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   }
 }
 
-template <int G, int NT>
+template <int G, int NT, bool F32>
 cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   using S = Shape<G, NT>;
   static std::atomic<uint64_t> ready{0};   // devices on which the shared-memory limit is raised
@@ -807,7 +827,7 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
-    if (const cudaError_t e = cudaFuncSetAttribute(moe_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (const cudaError_t e = cudaFuncSetAttribute(moe_kernel<G, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         e != cudaSuccess)
       return e;
     if (dev < 64) ready.fetch_or(bit, std::memory_order_relaxed);
@@ -825,7 +845,7 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT>, p);
+  return cudaLaunchKernelEx(&cfg, moe_kernel<G, NT, F32>, p);
 }
 
 // One column tile a job for few tokens, which leaves the ring longer: for 4-bit weights
@@ -834,8 +854,8 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
 // us, with two tiles 114; 8 tokens: 537 and 527 us).
 template <int G>
 cudaError_t launch_g(const MoeParams& p, int num_sms, cudaStream_t s) {
-  if (p.n <= (G != 0 ? 8 : 4)) return launch<G, 1>(p, num_sms, s);
-  return launch<G, 2>(p, num_sms, s);
+  if (p.n <= (G != 0 ? 8 : 4)) return p.out_f32 ? launch<G, 1, true>(p, num_sms, s) : launch<G, 1, false>(p, num_sms, s);
+  return p.out_f32 ? launch<G, 2, true>(p, num_sms, s) : launch<G, 2, false>(p, num_sms, s);
 }
 
 }  // namespace

@@ -287,7 +287,7 @@ int ep_moe_create(const ep_moe_cfg_t* cfg, ep_moe_t* out) noexcept {
     m->wait_ns = WaitLimitNs();
     const size_t entries = static_cast<size_t>(cfg->max_tokens) * cfg->num_expert_per_token;
     auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
-    const size_t n_h = up(entries * cfg->intermediate_dim * 4);
+    const size_t n_h = up(entries * cfg->intermediate_dim * 6);
     const size_t n_part = up(entries * cfg->hidden_dim * sizeof(float));
     const size_t n_tile = static_cast<size_t>(cfg->hidden_dim + 15) / 16;
     const size_t total = n_h + n_part + up(sizeof(int32_t) * (cfg->num_experts + n_tile + 2));

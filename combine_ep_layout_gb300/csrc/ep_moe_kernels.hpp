@@ -63,7 +63,7 @@ struct MoeParams {
   int act;
   bool out_f32;
   // workspace
-  void* h;                  // bf16 [max_tokens * K, 2, I]: the upper and the lower half of h
+  void* h;                  // bf16 [max_tokens * K, 2 or (fp32 output) 3, I]: the parts that h is the sum of
   float* part;              // [max_tokens * K, H]
   // counters, zero between launches
   int32_t* ready;           // [E] finished gate/up rounds by expert

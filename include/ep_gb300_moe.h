@@ -140,6 +140,7 @@ int ep_moe_create(const ep_moe_cfg_t *cfg, ep_moe_t *out) EP_NOEXCEPT;
 
 /* The experts of a few tokens: for every token t
  *   h[t][k]  = act(W1[e] x[t]) * (W3[e] x[t]),  e = topk_idx[t][k], rounded to 16 significant bits
+ *              (none of its 24 bits is dropped where out is fp32)
  *   out[t]   = sum over k ascending of topk_weights[t][k] * (W2[e] h[t][k])  (+ bias[t])
  * with fp32 sums; the expert rows W2 h stay fp32, the fold over k is the one
  * of ep_combine.  x: device bf16 [num_tokens, H]; topk_idx: device int64
