@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_chosen_kernel(Rout
     f = tot > 0.0f ? f / tot : 0.0f;
     d = f * (g - group_sum(id >= 0 ? g * f : 0.0f));
   }
-  if (p.sigmoid) d *= 1.0f - s;
+  if (p.sigmoid) d *= sigmoid(-zk);                       // 1 - s, with all its bits where s is near 1
   __syncwarp();                                           // the rows' writes come before the entries'
   if (id >= 0) static_cast<T*>(p.grad)[t * p.grad_stride + id] = from_float<T>(zk > -INFINITY ? d : 0.0f);
 }
