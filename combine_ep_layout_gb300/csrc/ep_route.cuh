@@ -13,7 +13,7 @@ constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ float warp_max(float v) {
   float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
 
