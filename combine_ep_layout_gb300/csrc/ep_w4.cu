@@ -325,11 +325,11 @@ __global__ void __launch_bounds__(Wide<G, NT>::kThreads, Wide<G, NT>::kPerSm) w4
 // (`together` each), in units of 10 ns.  A block's beginning and end cost as much as
 // `ends` stages, a cluster 1 us more.  At most the 8 blocks that a cluster may always
 // have.
-int choose_splits(int tiles, int stages, int alone, int together, int ends) {
+int choose_splits(int sms, int tiles, int stages, int alone, int together, int ends) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int s = 1; s <= 8 && s <= stages; s *= 2) {
-    const int64_t each = (stages + s - 1) / s + ends, per_sm = (static_cast<int64_t>(tiles) * s + 151) / 152;
+    const int64_t each = (stages + s - 1) / s + ends, per_sm = (static_cast<int64_t>(tiles) * s + sms - 1) / sms;
     int64_t cost = per_sm * together > alone ? per_sm * each * together : each * alone;
     if (s > 1) cost += 100;
     if (cost < least) least = cost, best = s;
@@ -337,11 +337,31 @@ int choose_splits(int tiles, int stages, int alone, int together, int ends) {
   return best;
 }
 
+// What the shape of a launch goes by, asked once for each device.
+struct Gpu {
+  int device, sms, smem_per_sm;
+};
+cudaError_t current_gpu(Gpu* g) {
+  static std::atomic<uint64_t> known[64];   // by device: SMs and bytes of an SM, 0: not asked yet
+  if (const cudaError_t e = cudaGetDevice(&g->device); e != cudaSuccess) return e;
+  if (g->device < 64) {
+    if (const uint64_t v = known[g->device].load(std::memory_order_relaxed); v != 0) {
+      g->sms = static_cast<int>(v >> 32), g->smem_per_sm = static_cast<int>(v & 0xffffffffu);
+      return cudaSuccess;
+    }
+  }
+  if (const cudaError_t e = cudaDeviceGetAttribute(&g->sms, cudaDevAttrMultiProcessorCount, g->device); e != cudaSuccess) return e;
+  if (const cudaError_t e = cudaDeviceGetAttribute(&g->smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, g->device);
+      e != cudaSuccess)
+    return e;
+  if (g->device < 64)
+    known[g->device].store(static_cast<uint64_t>(g->sms) << 32 | static_cast<uint32_t>(g->smem_per_sm), std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 template <class K>
-cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, const W4Params& p, int tiles, int splits, int threads,
+cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, int dev, const W4Params& p, int tiles, int splits, int threads,
                    int most_bytes, int bytes, cudaStream_t s) {
-  int dev = 0;
-  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
   // the kernel's shared-memory limit is raised once on each device
   const uint64_t bit = 1ull << (dev & 63);
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
@@ -376,11 +396,13 @@ cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
   using S = Narrow<G, NT>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + S::F::kRows - 1) / S::F::kRows, chunks = (p.cols + 127) / 128;
-  const int splits = choose_splits(tiles, (chunks + kWarps - 1) / kWarps, 60, 40, 3);
+  Gpu gpu;
+  if (const cudaError_t e = current_gpu(&gpu); e != cudaSuccess) return e;
+  const int splits = choose_splits(gpu.sms, tiles, (chunks + kWarps - 1) / kWarps, 60, 40, 3);
   // as many tiles at once as the blocks that fit together can take
-  const int by_bytes = 228 * 1024 / (S::bytes(p.n) + 1024);
-  const int most = 152 * (by_bytes < S::kFit ? by_bytes : S::kFit) / splits;
-  return launch(w4_narrow_kernel<G, NT>, ready, p, tiles < most ? tiles : most, splits, kThreads, S::bytes(8 * NT), S::bytes(p.n), s);
+  const int by_bytes = gpu.smem_per_sm / (S::bytes(p.n) + 1024);
+  const int blocks = gpu.sms * (by_bytes < S::kFit ? by_bytes : S::kFit), most = blocks > splits ? blocks / splits : 1;
+  return launch(w4_narrow_kernel<G, NT>, ready, gpu.device, p, tiles < most ? tiles : most, splits, kThreads, S::bytes(8 * NT), S::bytes(p.n), s);
 }
 
 template <int G, int NT>
@@ -388,8 +410,10 @@ cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
   using S = Wide<G, NT>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + S::kRows - 1) / S::kRows, chunks = (p.cols + 127) / 128;
-  return launch(w4_wide_kernel<G, NT>, ready, p, tiles, choose_splits(tiles, chunks, 90, 12 + 4 * NT, 4), S::kThreads, S::kBytes,
-                S::kBytes, s);
+  Gpu gpu;
+  if (const cudaError_t e = current_gpu(&gpu); e != cudaSuccess) return e;
+  return launch(w4_wide_kernel<G, NT>, ready, gpu.device, p, tiles, choose_splits(gpu.sms, tiles, chunks, 90, 12 + 4 * NT, 4),
+                S::kThreads, S::kBytes, S::kBytes, s);
 }
 
 // Where narrow and wide meet: 4096 x 14336, 8 tokens 11.2 us narrow, 18.0 wide; 16
