@@ -232,10 +232,12 @@ struct Wide {
   static constexpr int kXAt = kWarps * kWarpBytes;
   static constexpr int kSlot = kXAt + 8 * NT * F::kXBytes;
   static constexpr int kStages = 4;
-  // Blocks that fit together.  Up to 16 tokens 5: 20011 x 4096, 13 tokens, 21.4 us (4: 22.2,
-  // a few of its 626 blocks have to wait; 6: 27.0, too few registers); up to 32 tokens 4: 4096
-  // x 14336 23.4 us (5, with a stage less: 26.4); more: 2.
-  static constexpr int kPerSm = NT == 8 ? 2 : NT == 4 ? 4 : 5;
+  // Blocks that fit together.  With 5 up to 16 tokens registers get scarce: of eleven
+  // matrices, 13 tokens, groups of 64, six took 6 to 18% longer (7168 x 2048: 7.4 us, with 4
+  // 6.4; 4096 x 14336: 17.8 and 15.1; 16384 x 2048: 11.4 and 9.9), four were up to 5% faster
+  // (20011 x 4096: 20.1 and 21.1), with groups of 128 none differs by more than 2%.  Up to 32 tokens
+  // 4096 x 14336 takes 23 us with 4 and 26 with 5 and a stage less.  64 tokens leave room for 2.
+  static constexpr int kPerSm = NT == 8 ? 2 : 4;
   static constexpr int kRows = kWarps * F::kRows;
   static constexpr int kRed = 8 * NT * (kRows + 4) * 4;
   static constexpr int kBytes = kStages * kSlot > kRed ? kStages * kSlot : kRed;
@@ -324,7 +326,11 @@ __global__ void __launch_bounds__(Wide<G, NT>::kThreads, Wide<G, NT>::kPerSm) w4
 // one block's alone (`alone`, its latency) or all of an SM's blocks together
 // (`together` each), in units of 10 ns.  A block's beginning and end cost as much as
 // `ends` stages, a cluster 1 us more.  At most the 8 blocks that a cluster may always
-// have.
+// have.  Held against every number of blocks (1, 2, 4, 8) on eleven matrices from 512 x 1024
+// to 20011 x 4096 with 1 to 64 tokens, groups of 128: the choice is the fastest or within 9%
+// of it, but for 4096 x 4096 with up to 8 tokens (6.5 us, with two blocks 5.2), 1024 x 1024
+// with 12 to 32 (3.6 and 3.0 with four) and 7168 x 2048 with 64 (14.3 and 11.8 with two); one
+// block always takes up to 4.6 times as long (512 x 14336, 64 tokens).
 int choose_splits(int sms, int tiles, int stages, int alone, int together, int ends) {
   int best = 1;
   int64_t least = INT64_MAX;
