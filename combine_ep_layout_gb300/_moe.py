@@ -43,8 +43,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the current device's index without the lazy set-up, which a CUDA tensor has been through
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+# a call without a handle launches on the current device
+_NOT_CURRENT = "the tensors are not on the current device"
+
+
 def _stream(stream, index):
-    return _raw_stream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _raw_stream(index)
+    _require(stream.device_index == index, "the stream is not of the tensors' device")
+    return stream.cuda_stream
 
 
 _lib = None
@@ -74,8 +84,8 @@ def _load():
     return L
 
 
-def _is(t, dtype, shape):
-    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+def _is(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
 
 
 # ------------------------------------------------------------------ router
@@ -94,24 +104,21 @@ def _logits(cfg, logits, what):
     return logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), cfg.num_experts)
 
 
-def _route_args(cfg, logits, topk_idx, topk_weights, select_bias):
-    stride = _logits(cfg, logits, "logits")
-    shape = (logits.shape[0], cfg.topk)
-    _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
-    _require(_is(topk_weights, torch.float32, shape),
-             "topk_weights must be a contiguous fp32 CUDA tensor [n, topk]")
-    _require(select_bias is None or _is(select_bias, torch.float32, (cfg.num_experts,)),
-             "select_bias must be a contiguous fp32 CUDA tensor [num_experts]")
-    return stride
-
-
 def ep_route(cfg, logits, topk_idx, topk_weights, select_bias=None, stream=None):
     """Scores [n, E] (bf16 or fp32, contiguous rows at any row stride) to the
     topk_idx (int64) and topk_weights (fp32) [n, K] that layout and combine take."""
-    stride = _route_args(cfg, logits, topk_idx, topk_weights, select_bias)
+    stride = _logits(cfg, logits, "logits")
+    device, shape = logits.get_device(), (logits.shape[0], cfg.topk)
+    _require(device == _current_device(), _NOT_CURRENT)
+    _require(_is(topk_idx, torch.int64, shape, device),
+             "topk_idx must be a contiguous int64 CUDA tensor [n, topk] on the device of logits")
+    _require(_is(topk_weights, torch.float32, shape, device),
+             "topk_weights must be a contiguous fp32 CUDA tensor [n, topk] on the device of logits")
+    _require(select_bias is None or _is(select_bias, torch.float32, (cfg.num_experts,), device),
+             "select_bias must be a contiguous fp32 CUDA tensor [num_experts] on the device of logits")
     _check(_load().ep_route(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride, _ptr(select_bias),
                             logits.shape[0], topk_idx.data_ptr(), topk_weights.data_ptr(),
-                            _stream(stream, logits.get_device())))
+                            _stream(stream, device)))
 
 
 def ep_route_backward(cfg, logits, topk_idx, grad_weights, grad_logits, stream=None):
@@ -119,15 +126,17 @@ def ep_route_backward(cfg, logits, topk_idx, grad_weights, grad_logits, stream=N
     grad_logits [n, E] of the logits' type out (every element written)."""
     stride = _logits(cfg, logits, "logits")
     gstride = _logits(cfg, grad_logits, "grad_logits")
-    _require(grad_logits.dtype == logits.dtype and grad_logits.shape == logits.shape,
-             "grad_logits must have the type and shape of logits")
-    shape = (logits.shape[0], cfg.topk)
-    _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
-    _require(_is(grad_weights, torch.float32, shape),
-             "grad_weights must be a contiguous fp32 CUDA tensor [n, topk]")
+    device, shape = logits.get_device(), (logits.shape[0], cfg.topk)
+    _require(device == _current_device(), _NOT_CURRENT)
+    _require(grad_logits.dtype == logits.dtype and grad_logits.shape == logits.shape and
+             grad_logits.get_device() == device, "grad_logits must have the type, shape and device of logits")
+    _require(_is(topk_idx, torch.int64, shape, device),
+             "topk_idx must be a contiguous int64 CUDA tensor [n, topk] on the device of logits")
+    _require(_is(grad_weights, torch.float32, shape, device),
+             "grad_weights must be a contiguous fp32 CUDA tensor [n, topk] on the device of logits")
     _check(_load().ep_route_backward(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride,
                                      topk_idx.data_ptr(), grad_weights.data_ptr(), logits.shape[0],
-                                     grad_logits.data_ptr(), gstride, _stream(stream, logits.get_device())))
+                                     grad_logits.data_ptr(), gstride, _stream(stream, device)))
 
 
 # ----------------------------------------------------------- 4-bit weights
@@ -139,16 +148,19 @@ def ep_w4_linear(x, qweight, scales, out, stream=None):
     _require(x.dim() == 2 and qweight.dim() == 2 and scales.dim() == 2, "x, qweight and scales must be 2-D")
     n, cols = x.shape
     rows, groups = scales.shape
-    _require(_is(x, torch.bfloat16, (n, cols)), "x must be a contiguous bf16 CUDA tensor [n, cols]")
-    _require(cols % 2 == 0 and _is(qweight, torch.uint8, (rows, cols // 2)),
-             "qweight must be a contiguous uint8 CUDA tensor [rows, cols / 2]")
-    _require(groups > 0 and cols % groups == 0 and _is(scales, torch.float32, (rows, groups)),
-             "scales must be a contiguous fp32 CUDA tensor [rows, cols / group_size]")
-    _require(out.dtype in _FLOATS and _is(out, out.dtype, (n, rows)),
-             "out must be a contiguous bf16 or fp32 CUDA tensor [n, rows]")
+    device = x.get_device()
+    _require(x.dtype is torch.bfloat16 and device >= 0 and x.is_contiguous(),
+             "x must be a contiguous bf16 CUDA tensor [n, cols]")
+    _require(device == _current_device(), _NOT_CURRENT)
+    _require(cols % 2 == 0 and _is(qweight, torch.uint8, (rows, cols // 2), device),
+             "qweight must be a contiguous uint8 CUDA tensor [rows, cols / 2] on the device of x")
+    _require(groups > 0 and cols % groups == 0 and _is(scales, torch.float32, (rows, groups), device),
+             "scales must be a contiguous fp32 CUDA tensor [rows, cols / group_size] on the device of x")
+    _require(out.dtype in _FLOATS and _is(out, out.dtype, (n, rows), device),
+             "out must be a contiguous bf16 or fp32 CUDA tensor [n, rows] on the device of x")
     _check(_load().ep_w4_linear(x.data_ptr(), n, qweight.data_ptr(), scales.data_ptr(), rows, cols,
                                 cols // groups, out.data_ptr(), _FLOATS[out.dtype],
-                                _stream(stream, x.get_device())))
+                                _stream(stream, device)))
 
 
 # --------------------------------------------- MoE layer for a few tokens
@@ -168,9 +180,11 @@ class EpMoeWeights:
 
     def __init__(self, w13, w2, w13_scales=None, w2_scales=None):
         self.tensors = (w13, w2, w13_scales, w2_scales)
+        self.device = w13.get_device()
         for t in self.tensors:
             _require(t is None or (t.is_cuda and t.is_contiguous() and t.dim() == 3),
                      "weights and scales must be contiguous 3-D CUDA tensors")
+            _require(t is None or t.get_device() == self.device, "weights and scales must be on one device")
         _require((w13_scales is None) == (w2_scales is None),
                  "w13_scales and w2_scales come together")
         q = w13_scales is not None
@@ -216,16 +230,19 @@ class EpMoe:
         return self._m
 
     def _args(self, x, weights, topk_idx, topk_weights, out, bias):
-        n, cfg = x.shape[0], self.cfg
-        _require(_is(x, torch.bfloat16, (n, cfg.hidden_dim)), "x must be a contiguous bf16 CUDA tensor [n, hidden]")
+        n, cfg, device = x.shape[0], self.cfg, self.device
+        _require(_is(x, torch.bfloat16, (n, cfg.hidden_dim), device),
+                 "x must be a contiguous bf16 CUDA tensor [n, hidden] on the handle's device")
         shape = (n, cfg.num_expert_per_token)
-        _require(_is(topk_idx, torch.int64, shape), "topk_idx must be a contiguous int64 CUDA tensor [n, topk]")
-        _require(_is(topk_weights, torch.float32, shape),
-                 "topk_weights must be a contiguous fp32 CUDA tensor [n, topk]")
-        _require(out.dtype in _FLOATS and _is(out, out.dtype, x.shape),
-                 "out must be a contiguous bf16 or fp32 CUDA tensor [n, hidden]")
-        _require(bias is None or _is(bias, torch.bfloat16, x.shape),
-                 "bias must be a contiguous bf16 CUDA tensor [n, hidden]")
+        _require(_is(topk_idx, torch.int64, shape, device),
+                 "topk_idx must be a contiguous int64 CUDA tensor [n, topk] on the handle's device")
+        _require(_is(topk_weights, torch.float32, shape, device),
+                 "topk_weights must be a contiguous fp32 CUDA tensor [n, topk] on the handle's device")
+        _require(out.dtype in _FLOATS and _is(out, out.dtype, x.shape, device),
+                 "out must be a contiguous bf16 or fp32 CUDA tensor [n, hidden] on the handle's device")
+        _require(bias is None or _is(bias, torch.bfloat16, x.shape, device),
+                 "bias must be a contiguous bf16 CUDA tensor [n, hidden] on the handle's device")
+        _require(weights.device == device, "the weights are not on the handle's device")
         weights.check(cfg)
         return n
 
@@ -241,9 +258,10 @@ class EpMoe:
         """ep_route of logits into topk_idx and topk_weights, then forward with them."""
         n = self._args(x, weights, topk_idx, topk_weights, out, bias)
         stride = _logits(route_cfg, logits, "logits")
-        _require(logits.shape[0] == n, "logits must have a row for each row of x")
-        _require(select_bias is None or _is(select_bias, torch.float32, (route_cfg.num_experts,)),
-                 "select_bias must be a contiguous fp32 CUDA tensor [num_experts]")
+        _require(logits.shape[0] == n and logits.get_device() == self.device,
+                 "logits must have a row for each row of x, on its device")
+        _require(select_bias is None or _is(select_bias, torch.float32, (route_cfg.num_experts,), self.device),
+                 "select_bias must be a contiguous fp32 CUDA tensor [num_experts] on the handle's device")
         _check(_load().ep_moe_layer(self.ptr, route_cfg, x.data_ptr(), n, logits.data_ptr(),
                                     _FLOATS[logits.dtype], stride, _ptr(select_bias), weights.c,
                                     _ptr(bias), topk_idx.data_ptr(), topk_weights.data_ptr(),
