@@ -98,29 +98,26 @@ __device__ __forceinline__ void put_sums(float* red, int row0, int lane, const f
 
 // ------------------------------------------------------------------ narrow
 
-template <int G, int NT>
+template <int G>
 struct Narrow {
   static constexpr int kRowTiles = 2;
   using F = Form<G, kRowTiles>;
-  static constexpr int kStages = NT == 1 ? 3 : 2;
+  static constexpr int kStages = 3;
   static constexpr int kFit = 2;                                 // blocks that fit together
-  static constexpr int kWarpRed = 8 * NT * (F::kRows + 4);            // floats of one warp's sums
+  static constexpr int kWarpRed = 8 * (F::kRows + 4);            // floats of one warp's sums
   static constexpr int kRed = kWarps * kWarpRed * 4;
-  // the columns that no token fills are read (and not used) past the last slot
+  // a slot holds n columns; what a product reads of the others past the last slot (and does
+  // not use) are the sums
   static constexpr int slot(int n) { return F::kABytes + F::kSBytes + n * F::kXBytes; }
-  // (past the last one are the sums)
-  static constexpr int ring(int n) { return kWarps * kStages * slot(n); }
-  static constexpr int bytes(int n) {
-    const int over = (8 * NT - n) * F::kXBytes;
-    return ring(n) + (kRed > over ? kRed : over);
-  }
+  static constexpr int bytes(int n) { return kWarps * kStages * slot(n) + kRed; }
+  static_assert(kRed >= 8 * F::kXBytes);
 };
 
-template <int G, int NT>
-__global__ void __launch_bounds__(kThreads, Narrow<G, NT>::kFit) w4_narrow_kernel(const W4Params p, int splits) {
-  using S = Narrow<G, NT>;
+template <int G>
+__global__ void __launch_bounds__(kThreads, Narrow<G>::kFit) w4_narrow_kernel(const W4Params p, int splits) {
+  using S = Narrow<G>;
   using F = typename S::F;
-  constexpr int kStages = S::kStages, RT = S::kRowTiles;
+  constexpr int kStages = S::kStages, RT = S::kRowTiles, NT = 1;
   extern __shared__ __align__(128) uint8_t smem[];
   allow_dependent_grids();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -397,9 +394,9 @@ cudaError_t launch(K kernel, std::atomic<uint64_t>& ready, int dev, const W4Para
   return cudaLaunchKernelEx(&cfg, kernel, p, splits);
 }
 
-template <int G, int NT>
+template <int G>
 cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
-  using S = Narrow<G, NT>;
+  using S = Narrow<G>;
   static std::atomic<uint64_t> ready{0};
   const int tiles = (p.rows + S::F::kRows - 1) / S::F::kRows, chunks = (p.cols + 127) / 128;
   Gpu gpu;
@@ -408,7 +405,7 @@ cudaError_t launch_narrow(const W4Params& p, cudaStream_t s) {
   // as many tiles at once as the blocks that fit together can take
   const int by_bytes = gpu.smem_per_sm / (S::bytes(p.n) + 1024);
   const int blocks = gpu.sms * (by_bytes < S::kFit ? by_bytes : S::kFit), most = blocks > splits ? blocks / splits : 1;
-  return launch(w4_narrow_kernel<G, NT>, ready, gpu.device, p, tiles < most ? tiles : most, splits, kThreads, S::bytes(8 * NT), S::bytes(p.n), s);
+  return launch(w4_narrow_kernel<G>, ready, gpu.device, p, tiles < most ? tiles : most, splits, kThreads, S::bytes(8), S::bytes(p.n), s);
 }
 
 template <int G, int NT>
@@ -422,12 +419,14 @@ cudaError_t launch_wide(const W4Params& p, cudaStream_t s) {
                 S::kThreads, S::kBytes, S::kBytes, s);
 }
 
-// Where narrow and wide meet: 4096 x 14336, 8 tokens 11.2 us narrow, 18.0 wide; 16
-// tokens (narrow with two column tiles) 17.6 and 18.4, but 20011 x 4096 with 13 tokens
-// 25.0 and 21.4.
+// Where narrow and wide meet: with 8 tokens narrow is the faster one on all of eleven
+// matrices (4096 x 14336: 11.3 us, wide 16.9; 20011 x 4096: 14.8 and 19.4).  A narrow kernel
+// with two column tiles, which is not built, won with 13 tokens on nine (4096 x 14336: 13.5
+// and 17.1; 20011 x 4096: 18.3 and 19.6), with 16 it lost on the large ones (20011 x 4096:
+// 23.2 and 19.6).
 template <int G>
 cudaError_t launch_g(const W4Params& p, cudaStream_t s) {
-  if (p.n <= 8) return launch_narrow<G, 1>(p, s);
+  if (p.n <= 8) return launch_narrow<G>(p, s);
   if (p.n <= 16) return launch_wide<G, 2>(p, s);
   if (p.n <= 32) return launch_wide<G, 4>(p, s);
   return launch_wide<G, 8>(p, s);
