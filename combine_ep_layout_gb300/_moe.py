@@ -96,19 +96,22 @@ def make_route_cfg(num_experts, topk, score="softmax", renormalize=True, scale=1
 
 
 def _logits(cfg, logits, what):
-    _require(logits.is_cuda and logits.dim() == 2 and logits.shape[1] == cfg.num_experts and
-             logits.dtype in _FLOATS, "%s must be a bf16 or fp32 CUDA tensor [n, num_experts]" % what)
-    _require(logits.stride(1) == 1 or logits.shape[1] == 1 or logits.shape[0] == 0,
-             "%s must have contiguous rows" % what)
+    """Rows, row stride and device of scores or their gradient."""
+    device, shape, experts = logits.get_device(), logits.shape, cfg.num_experts
+    if device < 0 or len(shape) != 2 or shape[1] != experts or logits.dtype not in _FLOATS:
+        raise ValueError("%s must be a bf16 or fp32 CUDA tensor [n, num_experts]" % what)
+    n, stride = shape[0], logits.stride(0)
+    if logits.stride(1) != 1 and experts != 1 and n != 0:
+        raise ValueError("%s must have contiguous rows" % what)
     # a single row may carry any stride; rows may not overlap
-    return logits.stride(0) if logits.shape[0] > 1 else max(logits.stride(0), cfg.num_experts)
+    return n, stride if n > 1 else max(stride, experts), device
 
 
 def ep_route(cfg, logits, topk_idx, topk_weights, select_bias=None, stream=None):
     """Scores [n, E] (bf16 or fp32, contiguous rows at any row stride) to the
     topk_idx (int64) and topk_weights (fp32) [n, K] that layout and combine take."""
-    stride = _logits(cfg, logits, "logits")
-    device, shape = logits.get_device(), (logits.shape[0], cfg.topk)
+    n, stride, device = _logits(cfg, logits, "logits")
+    shape = (n, cfg.topk)
     _require(device == _current_device(), _NOT_CURRENT)
     _require(_is(topk_idx, torch.int64, shape, device),
              "topk_idx must be a contiguous int64 CUDA tensor [n, topk] on the device of logits")
@@ -117,25 +120,24 @@ def ep_route(cfg, logits, topk_idx, topk_weights, select_bias=None, stream=None)
     _require(select_bias is None or _is(select_bias, torch.float32, (cfg.num_experts,), device),
              "select_bias must be a contiguous fp32 CUDA tensor [num_experts] on the device of logits")
     _check(_load().ep_route(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride, _ptr(select_bias),
-                            logits.shape[0], topk_idx.data_ptr(), topk_weights.data_ptr(),
-                            _stream(stream, device)))
+                            n, topk_idx.data_ptr(), topk_weights.data_ptr(), _stream(stream, device)))
 
 
 def ep_route_backward(cfg, logits, topk_idx, grad_weights, grad_logits, stream=None):
     """Gradient of ep_route's topk_weights: grad_weights fp32 [n, K] in,
     grad_logits [n, E] of the logits' type out (every element written)."""
-    stride = _logits(cfg, logits, "logits")
-    gstride = _logits(cfg, grad_logits, "grad_logits")
-    device, shape = logits.get_device(), (logits.shape[0], cfg.topk)
+    n, stride, device = _logits(cfg, logits, "logits")
+    gn, gstride, gdevice = _logits(cfg, grad_logits, "grad_logits")
+    shape = (n, cfg.topk)
     _require(device == _current_device(), _NOT_CURRENT)
-    _require(grad_logits.dtype == logits.dtype and grad_logits.shape == logits.shape and
-             grad_logits.get_device() == device, "grad_logits must have the type, shape and device of logits")
+    _require(grad_logits.dtype is logits.dtype and gn == n and gdevice == device,
+             "grad_logits must have the type, shape and device of logits")
     _require(_is(topk_idx, torch.int64, shape, device),
              "topk_idx must be a contiguous int64 CUDA tensor [n, topk] on the device of logits")
     _require(_is(grad_weights, torch.float32, shape, device),
              "grad_weights must be a contiguous fp32 CUDA tensor [n, topk] on the device of logits")
     _check(_load().ep_route_backward(cfg, logits.data_ptr(), _FLOATS[logits.dtype], stride,
-                                     topk_idx.data_ptr(), grad_weights.data_ptr(), logits.shape[0],
+                                     topk_idx.data_ptr(), grad_weights.data_ptr(), n,
                                      grad_logits.data_ptr(), gstride, _stream(stream, device)))
 
 
@@ -257,8 +259,8 @@ class EpMoe:
               select_bias=None, stream=None):
         """ep_route of logits into topk_idx and topk_weights, then forward with them."""
         n = self._args(x, weights, topk_idx, topk_weights, out, bias)
-        stride = _logits(route_cfg, logits, "logits")
-        _require(logits.shape[0] == n and logits.get_device() == self.device,
+        rows, stride, device = _logits(route_cfg, logits, "logits")
+        _require(rows == n and device == self.device,
                  "logits must have a row for each row of x, on its device")
         _require(select_bias is None or _is(select_bias, torch.float32, (route_cfg.num_experts,), self.device),
                  "select_bias must be a contiguous fp32 CUDA tensor [num_experts] on the handle's device")
