@@ -38,13 +38,14 @@
 // tokens' rows took the latest block 120 us).  No sum depends on the order of blocks:
 // equal inputs, equal bits.
 //
-// Measured with the router before it, of a copy's 6.8 TB/s: bf16, 64 experts of 7168 x
-// 2048, top-8: 1 token 113 us (6.2 TB/s), 8 tokens 527 us (7.0 TB/s), 64 tokens 0.93 ms
+// Measured with the routing, of a copy's 6.8 TB/s: bf16, 64 experts of 7168 x
+// 2048, top-8: 1 token 113 us (6.2 TB/s), 8 tokens 527 us (7.0 TB/s), 64 tokens 0.92 ms
 // (6.1 TB/s: half the experts have more than the 8 tokens of a down job, so part of
 // w2 passes the SMs twice, at what L2 gives them).  4-bit, group 128, 128 experts of
-// 4096 x 1408, top-6: 8 tokens 103-108 us (3.6 TB/s), bound by instructions.  A layer of
-// 32 experts of 1024 x 512 takes 4 tokens 24 us: set-up 2.4, first weights 3.8, gate/up
-// 3.5, their fences 3, down 1.5, theirs and the fold 4.
+// 4096 x 1408, top-6: 8 tokens 104 us (3.6 TB/s) at 54% of the issue slots while active and
+// no unit above 44%: latency of 15 warps an SM.  A layer of 32 experts of 1024 x 512 takes 4
+// tokens 24 us: set-up 3.7, first weights 4.2, gate/up 3.5, their fences 3.4, down 1.3,
+// theirs and the fold 5.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -169,16 +170,16 @@ constexpr int lists_bytes(int entries) { return (entries * (4 + 4 + 2) + entries
 // HBM's full rate.
 template <int G, int NT>
 struct Shape {
-  // 4 row tiles spare 4-bit weights half the work on the activations (106 us, with 2
-  // 118 us: 8 tokens, 128 experts of 4096 x 1408); with 16 columns they would leave
-  // the ring too short
+  // 4 row tiles spare 4-bit weights half the work on the activations (105 us, with 2
+  // 116 us: 8 tokens, 128 experts of 4096 x 1408, groups of 128; with groups of 32 121 and
+  // 133); with 16 columns they would leave the ring too short
   static constexpr int kRowTiles = G != 0 && NT == 1 ? 4 : 2;
   // columns of one job: gate/up a token each, down as many for a token as it has parts
   static constexpr int kLogCap = NT == 1 ? 3 : 4, kCap = 1 << kLogCap;
   static constexpr int kEnough = 8, kItems = 4;              // stages of a warp in an item, items of a block (see widen)
   using F = Form<G, kRowTiles>;
-  // 4-bit weights take more instructions a byte: 12 warps (106 and 403 us for 8 and
-  // 64 tokens of those experts, with 8 warps 113 and 451 us)
+  // 4-bit weights take more instructions a byte: 12 warps (105 and 391 us for 8 and 64
+  // tokens of those experts, with 8 warps 114 and 451 us; groups of 32 and 64 the same to 1%)
   static constexpr int kWarps = G != 0 ? 12 : 8;
   static constexpr int kAllWarps = kWarps + kFinishers + 1;
   static constexpr int kThreads = 32 * kAllWarps;
@@ -355,8 +356,8 @@ __global__ void __launch_bounds__(Shape<G, NT>::kThreads, 1) moe_kernel(const Mo
   // An item is `wide` row tiles side by side, 1, 2 or 4, each with its share of the
   // warps: where the columns are few, one tile would give a warp so few stages that
   // setting them up costs more than they do (8 tokens, 128 4-bit experts of 4096 x
-  // 1408: 106 us, with one tile always 114; 64 tokens, 64 experts of 7168 x 2048: 0.94
-  // and 0.99 ms).  As long as every block keeps enough items for all to end together, and
+  // 1408: 105 us, with one tile always 114, 64 tokens 391 and 509; 64 tokens, 64 experts of
+  // 7168 x 2048: 0.91 and 0.98 ms).  As long as every block keeps enough items for all to end together, and
   // not for bf16 weights with an fp32 output: a warp's sums are then up to four times as
   // long, and the matrix instruction's additions round worse than fp32's (2048 x 1024, 64
   // tokens: off by 1.5e-6 of the output's norm, with one tile always 6.1e-7; 4-bit groups
@@ -849,9 +850,9 @@ cudaError_t launch(const MoeParams& p, int num_sms, cudaStream_t s) {
 }
 
 // One column tile a job for few tokens, which leaves the ring longer: for 4-bit weights
-// up to 8 tokens (128 experts of 4096 x 1408, 8 tokens: 106 us, with two tiles 140), for
-// bf16 up to the 4 that a down job then holds (64 experts of 7168 x 2048, 1 token: 112
-// us, with two tiles 114; 8 tokens: 537 and 527 us).
+// up to 8 tokens (128 experts of 4096 x 1408, 8 tokens: 105 us, with two tiles 137), for
+// bf16 up to the 4 that a down job then holds (64 experts of 7168 x 2048, 1 token: 111
+// us, with two tiles 113; 8 tokens: 528 and 519 us).
 template <int G>
 cudaError_t launch_g(const MoeParams& p, int num_sms, cudaStream_t s) {
   if (p.n <= (G != 0 ? 8 : 4)) return p.out_f32 ? launch<G, 1, true>(p, num_sms, s) : launch<G, 1, false>(p, num_sms, s);

@@ -11,18 +11,20 @@
 //       than fit, a block goes on to the next tile with its rings full.
 //   wide (9 to 64 tokens)    each of a block's 4 warps takes its own 16 rows and all
 //       share a stage's activations, which would outweigh the weights if every
-//       warp had its own.  Bound by the instructions that make operands of
-//       nibbles and by their latency, so the blocks are small and many.
+//       warp had its own.  Bound by the latency of making operands of nibbles and
+//       of a stage's barrier, so the blocks are small and many.
 //
 // Where the rows give too few blocks, a cluster of blocks shares a tile: each
 // takes its part of the columns, and the blocks' sums are added in rank order
 // through distributed shared memory.  No order is left to chance.
 //
-// Measured back to back (bytes of the weights, of a copy's 6.8 TB/s): 7168 x 7168, 1
-// token 9.4 us (2.9 TB/s); 20011 x 4096, 1 and 8 tokens 14.6 and 15.1 us (3.1 TB/s);
-// 4096 x 14336, 8, 16, 32 and 64 tokens 11.2, 18.4, 23.2 and 34.7 us.  Both are bound by
-// issuing instructions (28-32% of the slots over the kernel, half of them while the
-// warps have their data), the first few us of each by the first loads.
+// Measured one after the other in a graph, with weights that L2 does not hold, groups of
+// 128 (bytes of the weights, of a copy's 6.8 TB/s): 7168 x 7168, 1 token 10.1 us (2.7 TB/s);
+// 20011 x 4096, 1 and 8 tokens 14.4 and 14.8 us (3.0 TB/s); 4096 x 14336, 8, 16, 32 and 64
+// tokens 11.3, 17.2, 22.9 and 33.1 us.  No unit is saturated (7168 x 7168: 50% of the issue
+// slots while active, ALU 45%; 4096 x 14336, 32 tokens: 38%, 33%, tensor 30%): what is left is
+// latency, the first 2.6 us of each that of the first loads.  mma.sync alone would take
+// 4096 x 14336 6.2 us for 32 and 12.4 for 64 tokens.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
