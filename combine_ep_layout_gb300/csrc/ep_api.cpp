@@ -15,6 +15,7 @@
 #include <exception>
 #include <string>
 
+#include "ep_api_checks.hpp"
 #include "ep_cfg.hpp"
 #include "ep_gb300.h"
 #include "ep_jit.hpp"
@@ -161,6 +162,23 @@ int check_device(const ep_handle* h) {
     return fail(EP_EINVAL, "the current device is not the device the handle was created on");
   return EP_OK;
 }
+
+}  // namespace
+
+int epg::api::RoutingOf(ep_handle_t h, Routing* r) {
+  if (!h) return ::fail(EP_EINVAL, "handle is NULL");
+  if (const int rc = check_device(h); rc != EP_OK) return rc;
+  const ep_handle* o = owner(h);
+  *r = {o->num_tokens, o->K, o->E, h->H, o->rcap, o->no_expand, o->cnt, o->psum_expert, o->num_recv, o->send_slot, o->meta};
+  return EP_OK;
+}
+
+void epg::api::MarkUsed(ep_handle_t h, cudaStream_t s) {
+  h->last_stream = s;
+  h->launched = true;
+}
+
+namespace {
 
 // ep_handle_create (src null) and ep_handle_create_shared (src: the handle
 // whose layout the new one uses; nothing of the layout is allocated).

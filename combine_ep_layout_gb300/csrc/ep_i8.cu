@@ -1,0 +1,186 @@
+// ep_i8.cu -- rows to int8 with one scale each, in place of their tokens or to the
+// receive rows of a layout (include/ep_gb300_i8.h states the formulas).
+//
+// Bound by reading the rows once and writing what comes of them.  A group of
+// threads holds a row in registers between the search of its largest magnitude and the
+// rounding, so that x is read once; rows of more than 16384 columns are read a second time, out
+// of L2.  The magnitude is searched as an unsigned integer, where infinities and NaNs
+// are above every number.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "ep_i8_kernels.hpp"
+#include "ep_kernels.hpp"
+#include "ep_rows.cuh"
+#include "ep_types.cuh"
+
+namespace epg {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kVec = 16;      // columns of one vector: 16 bytes of int8
+constexpr int kMine = 2;      // vectors that a thread holds
+
+// 16 values of a row as floats.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void load16(const T* at, float (&v)[kVec]) {
+  if constexpr (ALIGNED) {
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kVec; i += kPer) {
+      const uint4 q = *reinterpret_cast<const uint4*>(at + i);
+      const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[i + j] = rows::as_float(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = rows::as_float(at[i]);
+  }
+}
+
+__device__ __forceinline__ unsigned magnitude(const float (&v)[kVec]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
+}
+
+// x / s rounded to the nearest integer, ties to even, four to a word.  x inv is off the
+// quotient (as fp32 rounds it) by less than 127 (2^-23 + 2^-24) < 2.3e-5, so where it is
+// further than 3e-5 from the middle of two integers both round alike; the others are
+// divided.  inv is no use where s is (nearly) subnormal.
+__device__ __forceinline__ uint4 round16(const float (&v)[kVec], float s, float inv) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer in the low bits
+  float r[kVec], off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const float t = v[i] * inv;
+    r[i] = t + kMagic;
+    off = fmaxf(off, fabsf(t - (r[i] - kMagic)));
+  }
+  if (!(off < 0.5f - 3e-5f) || !(s > 1e-30f)) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) r[i] = s > 0.0f ? fminf(fmaxf(__fdiv_rn(v[i], s), -127.0f), 127.0f) + kMagic : kMagic;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = __byte_perm(__float_as_uint(r[4 * i]), __float_as_uint(r[4 * i + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(r[4 * i + 2]), __float_as_uint(r[4 * i + 3]), 0x0040);
+    w[i] = __byte_perm(lo, hi, 0x5410);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// G threads a row, 128 / G rows a block where G is below 128.
+template <class T, int G, bool ALIGNED>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) i8_rows_kernel(I8RowsParams p) {
+  constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G;
+  __shared__ unsigned most[2][kThreads / 32];
+  allow_dependent_grids();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = threadIdx.x / G, at = threadIdx.x % G;
+  const int vectors = p.cols / kVec;
+  grid_dependency_wait();
+  const int64_t rows = p.num_recv ? ld_coherent(p.num_recv) : p.rows;
+  int turn = 0;
+  // uniform trip counts: a block's threads meet at the barrier of every turn
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+    const int64_t row = r0 + group;
+    const bool ok = row < rows && (!p.meta || ld_coherent(p.meta + row * p.meta_stride) >= 0);
+    const T* x = static_cast<const T*>(p.x) + row * p.row_stride;
+    float v[kMine][kVec];
+    unsigned m = 0;
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (ok && at + u * G < vectors) {
+        load16<T, ALIGNED>(x + static_cast<int64_t>(at + u * G) * kVec, v[u]);
+        m = max(m, magnitude(v[u]));
+      }
+    if (G == 512)
+      for (int c = at + kMine * G; ok && c < vectors; c += G) {
+        float more[kVec];
+        load16<T, ALIGNED>(x + static_cast<int64_t>(c) * kVec, more);
+        m = max(m, magnitude(more));
+      }
+    m = __reduce_max_sync(kAll, m);
+    if constexpr (G > 32) {
+      if (lane == 0) most[turn][warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) m = max(m, most[turn][group * (G / 32) + w]);
+    }
+    if (!ok) continue;
+    const bool fine = m < 0x7f800000u;
+    const float s = fine ? __fdiv_rn(__uint_as_float(m), 127.0f) : __uint_as_float(0x7fc00000u);
+    const float inv = fine ? 1.0f / s : 0.0f;
+    auto store = [&](int c, const float(&a)[kVec]) {
+      const uint4 q = fine ? round16(a, s, inv) : make_uint4(0, 0, 0, 0);
+      if (!p.slots) {
+        *reinterpret_cast<uint4*>(p.q + row * p.cols + static_cast<int64_t>(c) * kVec) = q;
+      } else {
+        for (int k = 0; k < p.topk; ++k) {
+          const int d = ld_coherent(p.slots + row * p.topk + k);
+          if (d >= 0) *reinterpret_cast<uint4*>(p.q + static_cast<int64_t>(d) * p.cols + static_cast<int64_t>(c) * kVec) = q;
+        }
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (at + u * G < vectors) store(at + u * G, v[u]);
+    if (G == 512)
+      for (int c = at + kMine * G; c < vectors; c += G) {
+        float more[kVec];
+        load16<T, ALIGNED>(x + static_cast<int64_t>(c) * kVec, more);
+        store(c, more);
+      }
+    if (!p.slots) {
+      if (at == 0) p.scales[row] = s;
+    } else {
+      for (int k = at; k < p.topk; k += G) {
+        const int d = ld_coherent(p.slots + row * p.topk + k);
+        if (d >= 0) p.scales[d] = s;
+      }
+    }
+  }
+}
+
+template <class T, int G>
+cudaError_t launch_g(const I8RowsParams& p, cudaStream_t s) {
+  constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G;
+  const bool vec = rows::aligned16(p.x, p.row_stride * static_cast<int64_t>(sizeof(T)));
+  const int64_t blocks = std::min<int64_t>((p.rows + kRows - 1) / kRows, p.num_recv ? 4096 : 1 << 24);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  static const bool pdl = PdlEnabled();
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return vec ? cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, true>, p) : cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, false>, p);
+}
+
+template <class T>
+cudaError_t launch(const I8RowsParams& p, cudaStream_t s) {
+  const int vectors = p.cols / kVec;
+  if (vectors <= 32 * kMine) return launch_g<T, 32>(p, s);
+  if (vectors <= 64 * kMine) return launch_g<T, 64>(p, s);
+  if (vectors <= 128 * kMine) return launch_g<T, 128>(p, s);
+  if (vectors <= 256 * kMine) return launch_g<T, 256>(p, s);
+  return launch_g<T, 512>(p, s);
+}
+
+}  // namespace
+
+cudaError_t LaunchI8Rows(const I8RowsParams& p, cudaStream_t s) {
+  if (p.rows == 0) return cudaSuccess;
+  return p.bf16 ? launch<__nv_bfloat16>(p, s) : launch<float>(p, s);
+}
+
+}  // namespace epg

@@ -23,45 +23,16 @@
 #include "ep_kernels.hpp"
 #include "ep_moe_kernels.hpp"
 #include "ep_route.cuh"
+#include "ep_rows.cuh"
 #include "ep_types.cuh"
 
 namespace epg {
 namespace {
 
 using namespace route;
+using namespace rows;
 
 constexpr int kWarps = 8;
-
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <class T>
-__device__ __forceinline__ T from_float(float v) {
-  if constexpr (sizeof(T) == 4)
-    return v;
-  else
-    return __float2bfloat16_rn(v);
-}
-
-// The V scores of a lane as floats; -inf past the end of the row and for NaN.
-template <class T, int V>
-__device__ __forceinline__ void load_row(const T* row, int experts, int lane, bool vec, float (&z)[V]) {
-  constexpr int kPer = 16 / sizeof(T);
-  const int j0 = lane * V;
-  if constexpr (V % kPer == 0) {
-    if (vec && j0 + V <= experts) {
-#pragma unroll
-      for (int v = 0; v < V; v += kPer) {
-        const uint4 q = *reinterpret_cast<const uint4*>(row + j0 + v);
-        const T* e = reinterpret_cast<const T*>(&q);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) z[v + i] = fmaxf(as_float(e[i]), -INFINITY);
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) z[v] = j0 + v < experts ? fmaxf(as_float(row[j0 + v]), -INFINITY) : -INFINITY;
-}
 
 // z becomes exp(z - peak); their sum over the row.
 template <int V>
@@ -120,29 +91,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteParams p, bool 
     p.idx[t * p.topk + lane] = chosen;
     p.weights[t * p.topk + lane] = chosen >= 0 ? f * p.scale : 0.0f;
   }
-}
-
-// A lane's V values of an output row.
-template <class T, int V>
-__device__ __forceinline__ void store_row(T* row, int experts, int lane, bool vec, const float (&z)[V]) {
-  constexpr int kPer = 16 / sizeof(T);
-  const int j0 = lane * V;
-  if constexpr (V % kPer == 0) {
-    if (vec && j0 + V <= experts) {
-#pragma unroll
-      for (int v = 0; v < V; v += kPer) {
-        uint4 q;
-        T* e = reinterpret_cast<T*>(&q);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) e[i] = from_float<T>(z[v + i]);
-        *reinterpret_cast<uint4*>(row + j0 + v) = q;
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (j0 + v < experts) row[j0 + v] = from_float<T>(z[v]);
 }
 
 // The gradient where it reaches every expert (softmax, not renormalised): a warp a
@@ -231,10 +179,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_chosen_kernel(Rout
   if (p.sigmoid) d *= sigmoid(-zk);                       // 1 - s, with all its bits where s is near 1
   __syncwarp();                                           // the rows' writes come before the entries'
   if (id >= 0) static_cast<T*>(p.grad)[t * p.grad_stride + id] = from_float<T>(zk > -INFINITY ? d : 0.0f);
-}
-
-bool aligned16(const void* p, int64_t stride_bytes) {
-  return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride_bytes)) & 15u) == 0;
 }
 
 template <class T, int V>
