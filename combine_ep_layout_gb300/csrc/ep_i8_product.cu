@@ -1,16 +1,39 @@
 // ep_i8_product.cu -- products of int8 rows with int8 weights, dense and grouped by
 // expert (include/ep_gb300_i8.h states the formulas).
 //
-// The simple form: a block of 256 threads takes 64 weight rows (gated: 32 gate rows and
-// their 32 up rows) and 64 rows of x, both staged in shared memory 64 columns at a
-// time, and adds four products an instruction (dp4a), exactly.
+// sm_103a has no integer tcgen05, and dp4a and integer mma.sync do 76 T multiply-adds a
+// second.  fp16 holds every int8 exactly and the 16-bit tensor cores do twelve times as
+// many, with products that are exact and fp32 sums that are exact below 2^24.  So both operands are
+// widened on the way: int8 travels from HBM and through L2 by TMA, and warps of the
+// multiplying SM turn it into fp16.
+//
+// A pair of CTAs takes 256 weight rows (128 each) and up to NT rows of x.  The weights
+// are the operand in tensor memory, where their fp16 form costs shared memory neither a write
+// nor a read; x is the operand in shared memory, each CTA widening half of it.  With the
+// weights along the 256 rows of the instruction, the number of tokens of a tile is free (a multiple of
+// 32), which experts with few tokens need.  Roles of a CTA's 20 warps:
+//   0       TMA loads of both operands, a ring of 128 columns a stage
+//   1       (first CTA) issues the products
+//   2       tensor memory
+//   4-11    widen: half of a stage's weight columns for 32 rows, and an eighth of x
+//   12-19   sums times scales, activation, output; up to 128 tokens the sums are double
+//           buffered, so that this runs beside the next tile
+// Gated: 64 gate rows and their 64 up rows make a CTA's 128; the warps that hold them
+// swap halves through shared memory.
+//
+// Every wait is bounded.  A warp that gives up records it, marks its CTA and leaves; the
+// others of the pair give up by the mark or by their own limit, and all meet before the
+// tensor memory is freed.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "ep_gb300_i8.h"
 #include "ep_i8_kernels.hpp"
+#include "ep_i8_mma.cuh"
 #include "ep_kernels.hpp"
 #include "ep_types.cuh"
 
@@ -19,82 +42,443 @@ namespace {
 
 __device__ int32_t g_error;
 
-constexpr int kTile = 64, kStep = 64, kPitch = kStep / 4 + 1;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 640, kWideners = 8, kWriters = 8;
+constexpr int kRows = 128;                 // weight rows of a CTA
+constexpr int kStep = 128;                 // columns of a stage
+constexpr int kColumnsA = kStep / 2;       // tensor memory columns of a stage's weights
+constexpr uint32_t kTmem = 512;
+constexpr int kMaxShared = 232448 - 1024 - 64;   // less what aligning the buffers may take, and static data
+
+__host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : 4; }   // widened stages
+__host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }         // sum buffers
+__host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
+__host__ __device__ constexpr int bytes_out(int nt) { return nt / 2 * kStep * 2; }
+constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over
+constexpr int kFixed = kWriters * kSwap + kWriters * 32 * 4 + 512;
+
+struct Args {
+  I8ProductParams p;
+  int steps;         // stages of a tile
+  int row_tiles;     // pair tiles along the weight rows
+  int stages_in;
+  CUtensorMap w, x;
+};
+
+struct Tile {
+  int expert, row_tile;
+  int64_t first;     // row of x
+  int tokens;        // rows of x that count
+  int width;         // columns of the product: a multiple of 32
+};
+
+// Expert e's rows go to the fewest tiles, of (nearly) one size each.
+__device__ __forceinline__ int token_tiles(int64_t count, int nt) { return static_cast<int>((count + nt - 1) / nt); }
+
+template <int NT>
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* starts, int tile) {
+  Tile t;
+  t.expert = 0;
+  if (a.p.first) {
+    int lo = 0, hi = a.p.experts;      // the last expert whose tiles begin at or before this one
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    t.expert = lo;
+    tile -= starts[lo];
+  }
+  const int64_t count = a.p.first ? ld_coherent(a.p.count + t.expert) : a.p.n;
+  const int tiles = token_tiles(count, NT), at = tile / a.row_tiles;
+  const int per = static_cast<int>(((count + tiles - 1) / tiles + 31) / 32) * 32;
+  t.row_tile = tile % a.row_tiles;
+  t.first = (a.p.first ? ld_coherent(a.p.first + t.expert) : 0) + static_cast<int64_t>(at) * per;
+  t.tokens = static_cast<int>(min(static_cast<int64_t>(per), count - static_cast<int64_t>(at) * per));
+  t.width = (t.tokens + 31) / 32 * 32;
+  return t;
+}
+
+// Waits of one CTA: false, and the CTA marked, when the limit has passed or the mark is there.
+struct Waits {
+  volatile int* dead;
+  uint64_t limit;
+
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (pair::try_wait(bar, parity)) return true;
+    const uint64_t t0 = tma::global_ns();
+    for (;;) {
+      if (*dead) return false;
+      if (limit != 0 && pair::try_wait(bar, parity)) return true;
+      if (limit == 0 || tma::global_ns() - t0 > limit) break;
+    }
+    *dead = 1;
+    atomicOr(&g_error, kErrTimeout);
+    return false;
+  }
+};
+
+// Four int8 as fp16: offset by 128 a byte is the low byte of 1024 + it, less 1152.
+__device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  v ^= 0x80808080u;
+  const __half2 base = __half2half2(__ushort_as_half(0x6480));
+  const uint32_t l = __byte_perm(v, 0x64646464u, 0x4140), h = __byte_perm(v, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), base), b = __hsub2(*reinterpret_cast<const __half2*>(&h), base);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 read16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void write16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
 __device__ __forceinline__ float activate(int act, float v) {
   if (act == EP_ACT_SILU) return v / (1.0f + expf(-v));
   return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * (v + 0.044715f * v * v * v)));
 }
 
-__global__ void __launch_bounds__(256) i8_simple_kernel(I8ProductParams p) {
-  __shared__ int ws[kTile][kPitch], xs[kTile][kPitch];
-  const int e = blockIdx.z, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const bool gated = p.act != EP_ACT_NONE;
-  const int half = p.rows / 2, out_rows = gated ? half : p.rows;
-  const int64_t first = p.first ? p.first[e] : 0, n = p.first ? p.count[e] : p.n;
-  // tile row i of this block's weights
-  auto weight_row = [&](int i) {
-    if (!gated) return static_cast<int>(blockIdx.x) * kTile + i;
-    const int r = static_cast<int>(blockIdx.x) * (kTile / 2) + i / 2;
-    return r < half ? (i & 1 ? half + r : r) : p.rows;
-  };
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.y) * kTile; t0 < n; t0 += static_cast<int64_t>(gridDim.y) * kTile) {
-    int acc[4][4] = {};
-    for (int c0 = 0; c0 < p.cols; c0 += kStep) {
-      __syncthreads();
-      const int i = threadIdx.x / 4, c = c0 + threadIdx.x % 4 * 16, wr = weight_row(i);
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (wr < p.rows && c < p.cols) a = *reinterpret_cast<const uint4*>(p.w + (static_cast<int64_t>(e) * p.rows + wr) * p.cols + c);
-      if (t0 + i < n && c < p.cols) b = *reinterpret_cast<const uint4*>(p.x + (first + t0 + i) * p.cols + c);
-      int* w = &ws[i][threadIdx.x % 4 * 4];
-      int* x = &xs[i][threadIdx.x % 4 * 4];
-      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-      x[0] = b.x, x[1] = b.y, x[2] = b.z, x[3] = b.w;
-      __syncthreads();
-#pragma unroll 4
-      for (int k = 0; k < kStep / 4; ++k) {
-        int u[4], v[4];
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_kernel(const __grid_constant__ Args a) {
+  constexpr int kTok = NT / 2, kIn = bytes_in(NT), kOut = bytes_out(NT), kS2 = stages_out(NT), kD = sums(NT);
+  constexpr uint32_t kSumColumns = kD * NT;
+  extern __shared__ uint8_t raw[];
+  __shared__ int dead;
+  __shared__ uint32_t tmem_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s1 = a.stages_in;
+  const uint32_t cta = pair::rank();
+  const uint32_t base = (tma::smem_u32(raw) + 1023) & ~1023u;
+  const uint32_t out0 = base + s1 * kIn, swap0 = out0 + kS2 * kOut, xs0 = swap0 + kWriters * kSwap, bars = xs0 + kWriters * 128;
+  int* starts = reinterpret_cast<int*>(raw + (bars + 512 - tma::smem_u32(raw)));
+  // barriers: s1 (at most 16) full, empty of the int8 ring; kS2 full, empty of the widened one; sums
+  // full, empty; swaps ready, done; end
+  const auto full_in = [&](int s) { return bars + 8 * s; };
+  const auto empty_in = [&](int s) { return bars + 128 + 8 * s; };
+  const auto full_out = [&](int s) { return bars + 256 + 8 * s; };
+  const auto empty_out = [&](int s) { return bars + 288 + 8 * s; };
+  const auto full_sum = [&](int s) { return bars + 320 + 8 * s; };
+  const auto empty_sum = [&](int s) { return bars + 336 + 8 * s; };
+  const auto swap_ready = [&](int s) { return bars + 352 + 8 * s; };
+  const auto swap_done = [&](int s) { return bars + 416 + 8 * s; };
+  const uint32_t end_bar = bars + 480;
+
+  if (threadIdx.x == 0) {
+    dead = 0;
+    for (int s = 0; s < s1; ++s) tma::mbar_init(full_in(s), 1), tma::mbar_init(empty_in(s), kWideners);
+    for (int s = 0; s < kS2; ++s) tma::mbar_init(full_out(s), 2 * kWideners), tma::mbar_init(empty_out(s), 1);
+    for (int s = 0; s < kD; ++s) tma::mbar_init(full_sum(s), 1), tma::mbar_init(empty_sum(s), 2 * kWriters);
+    for (int s = 0; s < kWriters; ++s) tma::mbar_init(swap_ready(s), 1), tma::mbar_init(swap_done(s), 1);
+    tma::mbar_init(end_bar, 1);
+    tma::mbar_init_fence();
+    pair::prefetch_map(&a.w);
+    pair::prefetch_map(&a.x);
+  }
+  if (warp == 2) {
+    pair::alloc(tma::smem_u32(&tmem_at), kTmem);
+    pair::relinquish();
+  }
+  allow_dependent_grids();
+  grid_dependency_wait();
+  int total;
+  if (a.p.first) {
+    // each expert's first tile, by a scan of warp 3's
+    if (warp == 3) {
+      int sum = 0;
+      for (int e0 = 0; e0 < a.p.experts; e0 += 32) {
+        const int e = e0 + lane;
+        const int mine = e < a.p.experts ? token_tiles(ld_coherent(a.p.count + e), NT) * a.row_tiles : 0;
+        int up = mine;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = ws[4 * tx + j][k], v[j] = xs[4 * ty + j][k];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int l = 0; l < 4; ++l) acc[j][l] = __dp4a(u[l], v[j], acc[j][l]);
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(kAll, up, d);
+          if (lane >= d) up += v;
+        }
+        if (e < a.p.experts) starts[e] = sum + up - mine;
+        sum += __shfl_sync(kAll, up, 31);
       }
-    }
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = t0 + 4 * ty + j;
-      if (t >= n) continue;
-      const float s = p.x_scales[first + t];
-      auto value = [&](int l) {
-        const int r = weight_row(4 * tx + l);
-        return r < p.rows ? static_cast<float>(acc[j][l]) * p.w_scales[static_cast<int64_t>(e) * p.rows + r] * s : 0.0f;
-      };
-      auto store = [&](int r, float y) {
-        const int64_t at = (first + t) * out_rows + r;
-        if (p.out_f32)
-          static_cast<float*>(p.out)[at] = y;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-      };
-      for (int l = 0; l < 4; ++l) {
-        const int r = weight_row(4 * tx + l);
-        if (!gated && r < p.rows) store(r, value(l));
-        if (gated && !(l & 1) && r < half) store(r, activate(p.act, value(l)) * value(l + 1));
-      }
+      if (lane == 0) starts[a.p.experts] = sum;
     }
   }
+  pair::fence_before();
+  __syncthreads();
+  pair::cluster_sync();
+  pair::fence_after();
+  total = a.p.first ? starts[a.p.experts] : token_tiles(a.p.n, NT) * a.row_tiles;
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(&tmem_at);
+  const Waits wait{&dead, a.p.wait_ns};
+  const int pairs = static_cast<int>(gridDim.x) / 2, first_tile = static_cast<int>(blockIdx.x) / 2;
+  const int half = a.p.rows / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < total; tile += pairs) {
+        const Tile t = tile_at<NT>(a, starts, tile);
+        const int64_t row0 = static_cast<int64_t>(t.expert) * a.p.rows;
+        const int lead = t.row_tile * (GATED ? kRows : 2 * kRows) + static_cast<int>(cta) * (GATED ? kRows / 2 : kRows);
+        const int y0 = static_cast<int>(row0 + lead), y1 = GATED ? y0 + half : y0 + kRows / 2;
+        const int yx = static_cast<int>(t.first) + static_cast<int>(cta) * (t.width / 2);
+        for (int k = 0; k < a.steps; ++k, ++it) {
+          const uint32_t s = it % s1, at = base + s * kIn;
+          if (!(ok = wait(empty_in(s), (it / s1 & 1) ^ 1))) break;
+          tma::mbar_expect_tx(full_in(s), kIn);
+          pair::load_box(at, &a.w, k * kStep, y0, full_in(s));
+          pair::load_box(at + kRows / 2 * kStep, &a.w, k * kStep, y1, full_in(s));
+          pair::load_box(at + kRows * kStep, &a.x, k * kStep, yx, full_in(s));
+        }
+      }
+      // the copies in flight land before the block ends
+      for (uint32_t j = it > static_cast<uint32_t>(s1) ? it - s1 : 0; j < it; ++j)
+        tma::mbar_wait_bounded(full_in(j % s1), j / s1 & 1, tma::kDrainNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && cta == 0) {
+      uint32_t it = 0, turn = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < total; tile += pairs, ++turn) {
+        const Tile t = tile_at<NT>(a, starts, tile);
+        const uint32_t buf = turn % kD, d = tmem + buf * NT, shape = pair::shape_f16(t.width);
+        if (!(ok = wait(empty_sum(buf), (turn / kD & 1) ^ 1))) break;
+        pair::fence_after();
+        for (int k = 0; k < a.steps; ++k, ++it) {
+          const uint32_t s = it % kS2;
+          if (!(ok = wait(full_out(s), it / kS2 & 1))) break;
+          pair::fence_after();
+          const int parts = min(kStep, a.p.cols - k * kStep) / 16;
+          const uint32_t at = tmem + kSumColumns + s * kColumnsA, b = out0 + s * kOut;
+          for (int i = 0; i < parts; ++i)
+            pair::mma(d, at + 8 * i, pair::operand(b + (i >> 2) * (kTok * 128) + (i & 3) * 32), shape, k + i != 0);
+          pair::commit(empty_out(s));
+        }
+        if (ok) pair::commit(full_sum(buf));
+      }
+      // the products in flight end before the tensor memory is freed
+      pair::commit_here(end_bar);
+      tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
+    }
+  } else if (warp >= 4 && warp < 4 + kWideners) {
+    const int w = warp - 4, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
+    const int thread = 32 * w + lane, xrow = thread % kTok, xpart = thread / kTok;
+    constexpr int kParts = 256 / kTok;          // threads of a row of x
+    const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * (kColumnsA / 2);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = first_tile; ok && tile < total; tile += pairs) {
+      for (int k = 0; k < a.steps; ++k, ++it) {
+        const uint32_t s = it % s1, s2 = it % kS2, at = base + s * kIn, atx = at + kRows * kStep;
+        ok = wait(full_in(s), it / s1 & 1) && wait(empty_out(s2), (it / kS2 & 1) ^ 1);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+        pair::fence_after();
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = read16(at + row * kStep + (((4 * part + c) ^ (row & 7)) << 4));
+          widen(v.x, r[8 * c], r[8 * c + 1]);
+          widen(v.y, r[8 * c + 2], r[8 * c + 3]);
+          widen(v.z, r[8 * c + 4], r[8 * c + 5]);
+          widen(v.w, r[8 * c + 6], r[8 * c + 7]);
+        }
+        pair::st32(to + s2 * kColumnsA, r);
+#pragma unroll
+        for (int c0 = 0; c0 < 8; c0 += kParts) {
+          const int c = c0 + xpart;
+          if (kParts > 8 && c >= 8) break;
+          const uint4 v = read16(atx + xrow * kStep + ((c ^ (xrow & 7)) << 4));
+          uint32_t q[8];
+          widen(v.x, q[0], q[1]);
+          widen(v.y, q[2], q[3]);
+          widen(v.z, q[4], q[5]);
+          widen(v.w, q[6], q[7]);
+          const uint32_t b = out0 + s2 * kOut + (c >> 2) * (kTok * 128) + xrow * 128;
+          const int c2 = 2 * (c & 3);
+          write16(b + ((c2 ^ (xrow & 7)) << 4), q[0], q[1], q[2], q[3]);
+          write16(b + (((c2 + 1) ^ (xrow & 7)) << 4), q[4], q[5], q[6], q[7]);
+        }
+        pair::fence_async();
+        pair::wait_st();
+        pair::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          tma::mbar_arrive(empty_in(s));
+          pair::arrive_remote(pair::in_cta(full_out(s2), 0));
+        }
+      }
+    }
+    // the last arrivals of the other CTA's products reach this one before it ends
+    if (ok && w == 0 && lane == 0)
+      for (uint32_t j = it > kS2 ? it - kS2 : 0; j < it; ++j) tma::mbar_wait_bounded(empty_out(j % kS2), j / kS2 & 1, tma::kDrainNs);
+  } else if (warp >= 12) {
+    const int w = warp - 12, quad = w & 3, which = w >> 2, other = w ^ 2;
+    const int out_rows = GATED ? half : a.p.rows;
+    float* xs = reinterpret_cast<float*>(raw + (xs0 + w * 128 - tma::smem_u32(raw)));
+    const auto swap_at = [&](int v) { return reinterpret_cast<float*>(raw + (swap0 + v * kSwap - tma::smem_u32(raw))); };
+    uint32_t turn = 0, swaps = 0;
+    bool ok = true;
+    for (int tile = first_tile; ok && tile < total; tile += pairs, ++turn) {
+      const Tile t = tile_at<NT>(a, starts, tile);
+      const uint32_t buf = turn % kD;
+      // the row of w that this lane holds, and its row in the output
+      int row, channel;
+      if (GATED) {
+        channel = t.row_tile * kRows + static_cast<int>(cta) * (kRows / 2) + 32 * (quad & 1) + lane;
+        row = quad < 2 ? channel : half + channel;
+      } else {
+        row = channel = t.row_tile * 2 * kRows + static_cast<int>(cta) * kRows + 32 * quad + lane;
+      }
+      const bool live = channel < out_rows;
+      const float ws = live ? ld_coherent(a.p.w_scales + static_cast<int64_t>(t.expert) * a.p.rows + row) : 0.0f;
+      ok = __all_sync(kAll, wait(full_sum(buf), turn / kD & 1));
+      if (!ok) break;
+      pair::fence_after();
+      for (int c = 32 * which; c < t.width; c += 64) {
+        uint32_t r[32];
+        pair::ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * NT + c, r);
+        __syncwarp();
+        xs[lane] = c + lane < t.tokens ? ld_coherent(a.p.x_scales + t.first + c + lane) : 0.0f;
+        __syncwarp();
+        pair::wait_ld();
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) * ws * xs[j];
+        const auto store = [&](int j, float v) {
+          if (live && c + j < t.tokens) {
+            const int64_t at = (t.first + c + j) * out_rows + channel;
+            if (a.p.out_f32)
+              static_cast<float*>(a.p.out)[at] = v;
+            else
+              static_cast<__nv_bfloat16*>(a.p.out)[at] = __float2bfloat16_rn(v);
+          }
+        };
+        if constexpr (GATED) {
+          // gate warps finish the first 16 tokens, up warps the last 16
+          float* mine = swap_at(w);
+          const float* theirs = swap_at(other);
+          const bool gate = quad < 2;
+          ok = __all_sync(kAll, wait(swap_done(w), (swaps & 1) ^ 1));
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mine[32 * j + lane] = gate ? y[16 + j] : y[j];
+          __syncwarp();
+          if (lane == 0) tma::mbar_arrive(swap_ready(w));
+          ok = __all_sync(kAll, wait(swap_ready(other), swaps & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float v = theirs[32 * j + lane];
+            store(gate ? j : 16 + j, gate ? activate(a.p.act, y[j]) * v : activate(a.p.act, v) * y[16 + j]);
+          }
+          __syncwarp();
+          if (lane == 0) tma::mbar_arrive(swap_done(other));
+          ++swaps;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) store(j, y[j]);
+        }
+      }
+      if (!ok) break;
+      pair::fence_before();
+      __syncwarp();
+      if (lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));
+    }
+  }
+  __syncwarp();
+  pair::fence_before();
+  __syncthreads();
+  pair::cluster_sync();
+  pair::fence_after();
+  if (warp == 2) pair::dealloc(tmem, kTmem);
+}
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+  static const Encode f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return f;
+}
+
+// Boxes of 128 columns by `box` rows of an int8 matrix; zeros outside it.
+cudaError_t map_of(CUtensorMap* map, const void* at, int64_t rows, int cols, int box) {
+  const Encode f = encoder();
+  if (!f) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)}, pitch[1] = {dims[0]};
+  const cuuint32_t boxes[2] = {kStep, static_cast<cuuint32_t>(box)}, steps[2] = {1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(at), dims, pitch, boxes, steps,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int NT, bool GATED>
+cudaError_t launch(Args& a, int num_sms, int64_t most_tiles, cudaStream_t s) {
+  const int starts = a.p.first ? 4 * (a.p.experts + 1) : 0;
+  const int room = kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - starts;
+  a.stages_in = std::min(16, room / bytes_in(NT));
+  const int smem = 1024 + a.stages_in * bytes_in(NT) + stages_out(NT) * bytes_out(NT) + kFixed + starts;
+  if (const cudaError_t e = map_of(&a.x, a.p.x, a.p.n, a.p.cols, NT / 2); e != cudaSuccess) return e;
+  if (const cudaError_t e = cudaFuncSetAttribute(i8_mma_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(num_sms / 2, most_tiles)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  static const bool pdl = PdlEnabled();
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, i8_mma_kernel<NT, GATED>, a);
 }
 
 }  // namespace
 
 cudaError_t LaunchI8Product(const I8ProductParams& p, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
-  const int out_rows = p.act == EP_ACT_NONE ? p.rows : p.rows / 2, per = p.act == EP_ACT_NONE ? kTile : kTile / 2;
-  const int64_t tiles = (p.n + kTile - 1) / kTile;
-  const dim3 grid((out_rows + per - 1) / per, static_cast<unsigned>(p.first ? 4 : tiles < 4096 ? tiles : 4096), p.experts);
-  i8_simple_kernel<<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  int dev = 0, sms = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  if (const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev); e != cudaSuccess) return e;
+  const bool gated = p.act != EP_ACT_NONE;
+  Args a{};
+  a.p = p;
+  a.steps = (p.cols + kStep - 1) / kStep;
+  a.row_tiles = gated ? (p.rows / 2 + kRows - 1) / kRows : (p.rows + 2 * kRows - 1) / (2 * kRows);
+  if (const cudaError_t e = map_of(&a.w, p.w, static_cast<int64_t>(p.experts) * p.rows, p.cols, kRows / 2); e != cudaSuccess)
+    return e;
+  // the tile's tokens: the average expert's rows, and some more, in as few tiles as that allows
+  const int64_t mean = p.first ? p.entries / p.experts + 1 : p.n;
+  const int nt = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : 256;
+  const int64_t most = static_cast<int64_t>(a.row_tiles) * (p.first ? std::min<int64_t>(p.entries, p.experts + p.entries / nt)
+                                                                    : (p.n + nt - 1) / nt);
+  if (gated) {
+    if (nt == 32) return launch<32, true>(a, sms, most, s);
+    if (nt == 64) return launch<64, true>(a, sms, most, s);
+    if (nt == 128) return launch<128, true>(a, sms, most, s);
+    return launch<256, true>(a, sms, most, s);
+  }
+  if (nt == 32) return launch<32, false>(a, sms, most, s);
+  if (nt == 64) return launch<64, false>(a, sms, most, s);
+  if (nt == 128) return launch<128, false>(a, sms, most, s);
+  return launch<256, false>(a, sms, most, s);
 }
 
 cudaError_t ReadI8Error(int32_t* value, cudaStream_t s) {
