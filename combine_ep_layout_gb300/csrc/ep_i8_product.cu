@@ -11,12 +11,14 @@
 // are the operand in tensor memory, where their fp16 form costs shared memory neither a write
 // nor a read; x is the operand in shared memory, each CTA widening half of it.  With the
 // weights along the 256 rows of the instruction, the number of tokens of a tile is free (a multiple of
-// 32), which experts with few tokens need.  Roles of a CTA's 20 warps:
+// 32), which experts with few tokens need.  Roles of a CTA's 28 warps:
 //   0       TMA loads of both operands, a ring of 128 columns a stage
 //   1       (first CTA) issues the products
 //   2       tensor memory
-//   4-11    widen: half of a stage's weight columns for 32 rows, and an eighth of x
-//   12-19   sums times scales, activation, output; up to 128 tokens the sums are double
+//   4-19    widen, 8 warps a stage and the two eights in turn, as a stage's latency (reads, fence,
+//           tensor memory, barriers) is twice its work: half of a stage's weight columns for
+//           32 rows, and an eighth of x
+//   20-27   sums times scales, activation, output; up to 128 tokens the sums are double
 //           buffered, so that this runs beside the next tile
 // Gated: 64 gate rows and their 64 up rows make a CTA's 128; the warps that hold them
 // swap halves through shared memory.
@@ -43,7 +45,8 @@ namespace {
 __device__ int32_t g_error;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 640, kWideners = 8, kWriters = 8;
+constexpr int kWideners = 8, kGroups = 2, kWriters = 8;   // warps of a stage, groups of them; writing warps
+constexpr int kFirstWriter = 4 + kWideners * kGroups, kThreads = 32 * (kFirstWriter + kWriters);
 constexpr int kRows = 128;                 // weight rows of a CTA
 constexpr int kStep = 128;                 // columns of a stage
 constexpr int kColumnsA = kStep / 2;       // tensor memory columns of a stage's weights
@@ -263,60 +266,74 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       pair::commit_here(end_bar);
       tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
     }
-  } else if (warp >= 4 && warp < 4 + kWideners) {
-    const int w = warp - 4, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
+  } else if (warp >= 4 && warp < kFirstWriter) {
+    const int w = (warp - 4) % kWideners, group = (warp - 4) / kWideners, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
     const int thread = 32 * w + lane, xrow = thread % kTok, xpart = thread / kTok;
-    constexpr int kParts = 256 / kTok;          // threads of a row of x
+    constexpr int kParts = 256 / kTok, kMine = kParts < 8 ? 8 / kParts : 1;   // threads of a row of x, its chunks of a thread
+    const bool has_x = xpart < 8;
     const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * (kColumnsA / 2);
-    uint32_t it = 0;
+    const uint32_t from_a = base + row * kStep, from_x = base + kRows * kStep + xrow * kStep;
+    const uint32_t to_x = out0 + xrow * 128;
+    // the group's stage of either ring, and the parity of its turn there
+    int in = group, out = group;
+    uint32_t in_turn = 0, out_turn = 0;
+    const int64_t all = first_tile < total ? static_cast<int64_t>((total - first_tile + pairs - 1) / pairs) * a.steps : 0;
     bool ok = true;
-    for (int tile = first_tile; ok && tile < total; tile += pairs) {
-      for (int k = 0; k < a.steps; ++k, ++it) {
-        const uint32_t s = it % s1, s2 = it % kS2, at = base + s * kIn, atx = at + kRows * kStep;
-        ok = wait(full_in(s), it / s1 & 1) && wait(empty_out(s2), (it / kS2 & 1) ^ 1);
-        ok = __all_sync(kAll, ok);
-        if (!ok) break;
-        pair::fence_after();
-        uint32_t r[32];
+    for (int64_t it = group; it < all; it += kGroups) {
+      // In this order: where the int8 ring has an odd number of stages the groups take turns on
+      // each of them, and the parity alone cannot tell the copy meant from one before the last.  The
+      // products of kS2 stages ago are done here, so the copy before is behind (s1 >= kS2).
+      ok = __all_sync(kAll, wait(empty_out(out), out_turn ^ 1) && wait(full_in(in), in_turn));
+      if (!ok) break;
+      pair::fence_after();
+      uint4 va[4], vx[kMine];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 v = read16(at + row * kStep + (((4 * part + c) ^ (row & 7)) << 4));
-          widen(v.x, r[8 * c], r[8 * c + 1]);
-          widen(v.y, r[8 * c + 2], r[8 * c + 3]);
-          widen(v.z, r[8 * c + 4], r[8 * c + 5]);
-          widen(v.w, r[8 * c + 6], r[8 * c + 7]);
-        }
-        pair::st32(to + s2 * kColumnsA, r);
+      for (int c = 0; c < 4; ++c) va[c] = read16(from_a + in * kIn + (((4 * part + c) ^ (row & 7)) << 4));
 #pragma unroll
-        for (int c0 = 0; c0 < 8; c0 += kParts) {
-          const int c = c0 + xpart;
-          if (kParts > 8 && c >= 8) break;
-          const uint4 v = read16(atx + xrow * kStep + ((c ^ (xrow & 7)) << 4));
-          uint32_t q[8];
-          widen(v.x, q[0], q[1]);
-          widen(v.y, q[2], q[3]);
-          widen(v.z, q[4], q[5]);
-          widen(v.w, q[6], q[7]);
-          const uint32_t b = out0 + s2 * kOut + (c >> 2) * (kTok * 128) + xrow * 128;
-          const int c2 = 2 * (c & 3);
-          write16(b + ((c2 ^ (xrow & 7)) << 4), q[0], q[1], q[2], q[3]);
-          write16(b + (((c2 + 1) ^ (xrow & 7)) << 4), q[4], q[5], q[6], q[7]);
+      for (int i = 0; i < kMine; ++i)
+        if (has_x) vx[i] = read16(from_x + in * kIn + (((xpart + i * kParts) ^ (xrow & 7)) << 4));
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          widen(va[c + i].x, r[8 * i], r[8 * i + 1]);
+          widen(va[c + i].y, r[8 * i + 2], r[8 * i + 3]);
+          widen(va[c + i].z, r[8 * i + 4], r[8 * i + 5]);
+          widen(va[c + i].w, r[8 * i + 6], r[8 * i + 7]);
         }
-        pair::fence_async();
-        pair::wait_st();
-        pair::fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          tma::mbar_arrive(empty_in(s));
-          pair::arrive_remote(pair::in_cta(full_out(s2), 0));
-        }
+        pair::st16(to + out * kColumnsA + 8 * c, r);
       }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (has_x) {
+          const int c = xpart + i * kParts, c2 = 2 * (c & 3);
+          uint32_t q[8];
+          widen(vx[i].x, q[0], q[1]);
+          widen(vx[i].y, q[2], q[3]);
+          widen(vx[i].z, q[4], q[5]);
+          widen(vx[i].w, q[6], q[7]);
+          const uint32_t at = to_x + out * kOut + (c >> 2) * (kTok * 128);
+          write16(at + ((c2 ^ (xrow & 7)) << 4), q[0], q[1], q[2], q[3]);
+          write16(at + (((c2 + 1) ^ (xrow & 7)) << 4), q[4], q[5], q[6], q[7]);
+        }
+      pair::fence_async();
+      pair::wait_st();
+      pair::fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tma::mbar_arrive(empty_in(in));
+        pair::arrive_remote(pair::in_cta(full_out(out), 0));
+      }
+      if ((in += kGroups) >= s1) in -= s1, in_turn ^= 1;
+      if ((out += kGroups) >= kS2) out -= kS2, out_turn ^= 1;
     }
     // the last arrivals of the other CTA's products reach this one before it ends
     if (ok && w == 0 && lane == 0)
-      for (uint32_t j = it > kS2 ? it - kS2 : 0; j < it; ++j) tma::mbar_wait_bounded(empty_out(j % kS2), j / kS2 & 1, tma::kDrainNs);
-  } else if (warp >= 12) {
-    const int w = warp - 12, quad = w & 3, which = w >> 2, other = w ^ 2;
+      for (int64_t j = all > kS2 ? all - kS2 : 0; j < all; ++j)
+        tma::mbar_wait_bounded(empty_out(static_cast<int>(j % kS2)), static_cast<uint32_t>(j / kS2) & 1, tma::kDrainNs);
+  } else if (warp >= kFirstWriter) {
+    const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;
     const int out_rows = GATED ? half : a.p.rows;
     float* xs = reinterpret_cast<float*>(raw + (xs0 + w * 128 - tma::smem_u32(raw)));
     const auto swap_at = [&](int v) { return reinterpret_cast<float*>(raw + (swap0 + v * kSwap - tma::smem_u32(raw))); };
@@ -431,6 +448,7 @@ cudaError_t launch(Args& a, int num_sms, int64_t most_tiles, cudaStream_t s) {
   const int starts = a.p.first ? 4 * (a.p.experts + 1) : 0;
   const int room = kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - starts;
   a.stages_in = std::min(16, room / bytes_in(NT));
+  static_assert((kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - 4 * 2049) / bytes_in(NT) >= stages_out(NT));
   const int smem = 1024 + a.stages_in * bytes_in(NT) + stages_out(NT) * bytes_out(NT) + kFixed + starts;
   if (const cudaError_t e = map_of(&a.x, a.p.x, a.p.n, a.p.cols, NT / 2); e != cudaSuccess) return e;
   if (const cudaError_t e = cudaFuncSetAttribute(i8_mma_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
