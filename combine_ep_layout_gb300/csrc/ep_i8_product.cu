@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   extern __shared__ uint8_t raw[];
   __shared__ int dead;
   __shared__ uint32_t tmem_at;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s1 = a.stages_in;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kAll, static_cast<int>(threadIdx.x >> 5), 0), s1 = a.stages_in;
   const uint32_t cta = pair::rank();
   const uint32_t base = (tma::smem_u32(raw) + 1023) & ~1023u;
   const uint32_t out0 = base + s1 * kIn, swap0 = out0 + kS2 * kOut, xs0 = swap0 + kWriters * kSwap, bars = xs0 + kWriters * 128;
@@ -242,28 +242,40 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
         tma::mbar_wait_bounded(full_in(j % s1), j / s1 & 1, tma::kDrainNs);
     }
   } else if (warp == 1) {
-    if (lane == 0 && cta == 0) {
-      uint32_t it = 0, turn = 0;
+    if (cta == 0) {
+      // the whole warp goes along, and one lane that the compiler knows to be one issues: the operands
+      // stay in uniform registers (27 cycles a product of 32 tokens, 136 of 256; by `lane == 0` 94 at least)
+      const bool one = pair::elect();
+      int stage = 0, buf = 0;
+      uint32_t stage_turn = 0, buf_turn = 0;
       bool ok = true;
-      for (int tile = first_tile; ok && tile < total; tile += pairs, ++turn) {
+      for (int tile = first_tile; ok && tile < total; tile += pairs) {
         const Tile t = tile_at<NT>(a, starts, tile);
-        const uint32_t buf = turn % kD, d = tmem + buf * NT, shape = pair::shape_f16(t.width);
-        if (!(ok = wait(empty_sum(buf), (turn / kD & 1) ^ 1))) break;
+        const uint32_t d = tmem + buf * NT, shape = pair::shape_f16(t.width);
+        if (!(ok = __all_sync(kAll, wait(empty_sum(buf), buf_turn ^ 1)))) break;
         pair::fence_after();
-        for (int k = 0; k < a.steps; ++k, ++it) {
-          const uint32_t s = it % kS2;
-          if (!(ok = wait(full_out(s), it / kS2 & 1))) break;
+        for (int k = 0; k < a.steps; ++k) {
+          if (!(ok = __all_sync(kAll, wait(full_out(stage), stage_turn)))) break;
           pair::fence_after();
           const int parts = min(kStep, a.p.cols - k * kStep) / 16;
-          const uint32_t at = tmem + kSumColumns + s * kColumnsA, b = out0 + s * kOut;
-          for (int i = 0; i < parts; ++i)
-            pair::mma(d, at + 8 * i, pair::operand(b + (i >> 2) * (kTok * 128) + (i & 3) * 32), shape, k + i != 0);
-          pair::commit(empty_out(s));
+          const uint32_t at = tmem + kSumColumns + stage * kColumnsA;
+          const uint64_t b = pair::operand(out0 + stage * kOut);
+          if (one) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < parts) pair::mma(d, at + 8 * i, b + (((i >> 2) * (kTok * 128) + (i & 3) * 32) >> 4), shape, k + i != 0);
+            pair::commit(empty_out(stage));
+          }
+          __syncwarp();
+          if (++stage == kS2) stage = 0, stage_turn ^= 1;
         }
-        if (ok) pair::commit(full_sum(buf));
+        if (ok && one) pair::commit(full_sum(buf));
+        __syncwarp();
+        if (++buf == kD) buf = 0, buf_turn ^= 1;
       }
       // the products in flight end before the tensor memory is freed
-      pair::commit_here(end_bar);
+      if (one) pair::commit_here(end_bar);
+      __syncwarp();
       tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
     }
   } else if (warp >= 4 && warp < kFirstWriter) {
