@@ -58,7 +58,8 @@ __host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }    
 __host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
 __host__ __device__ constexpr int bytes_out(int nt) { return nt / 2 * kStep * 2; }
 constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over
-constexpr int kFixed = kWriters * kSwap + kWriters * 32 * 4 + 512;
+constexpr int kScaleBytes = 4 * 32 * 4;    // a writing warp's scales of x
+constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + 512;
 
 struct Args {
   I8ProductParams p;
@@ -142,9 +143,27 @@ __device__ __forceinline__ void write16(uint32_t addr, uint32_t a, uint32_t b, u
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// v sigmoid(s): silu with s = v; the tanh form of gelu is the same with
+// s = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh(u)) / 2 is sigmoid(2 u).
 __device__ __forceinline__ float activate(int act, float v) {
-  if (act == EP_ACT_SILU) return v / (1.0f + expf(-v));
-  return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * (v + 0.044715f * v * v * v)));
+  const float s = act == EP_ACT_SILU ? v : v * fmaf(0.07135481282553f * v, v, 1.5957691216057308f);
+  return __fdividef(v, 1.0f + expf(-s));
+}
+
+// A lane's channel of the first `many` of N tokens.
+template <int N>
+__device__ __forceinline__ void store_column(const I8ProductParams& p, int64_t at, int pitch, int many, const float (&y)[N]) {
+  if (p.out_f32) {
+    float* out = static_cast<float*>(p.out) + at;
+#pragma unroll
+    for (int j = 0; j < N; ++j, out += pitch)
+      if (j < many) *out = y[j];
+  } else {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+    for (int j = 0; j < N; ++j, out += pitch)
+      if (j < many) *out = __float2bfloat16_rn(y[j]);
+  }
 }
 
 template <int NT, bool GATED>
@@ -157,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   const int lane = threadIdx.x & 31, warp = __shfl_sync(kAll, static_cast<int>(threadIdx.x >> 5), 0), s1 = a.stages_in;
   const uint32_t cta = pair::rank();
   const uint32_t base = (tma::smem_u32(raw) + 1023) & ~1023u;
-  const uint32_t out0 = base + s1 * kIn, swap0 = out0 + kS2 * kOut, xs0 = swap0 + kWriters * kSwap, bars = xs0 + kWriters * 128;
+  const uint32_t out0 = base + s1 * kIn, swap0 = out0 + kS2 * kOut, xs0 = swap0 + kWriters * kSwap, bars = xs0 + kWriters * kScaleBytes;
   int* starts = reinterpret_cast<int*>(raw + (bars + 512 - tma::smem_u32(raw)));
   // barriers: s1 (at most 16) full, empty of the int8 ring; kS2 full, empty of the widened one; sums
   // full, empty; swaps ready, done; end
@@ -347,75 +366,79 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   } else if (warp >= kFirstWriter) {
     const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;
     const int out_rows = GATED ? half : a.p.rows;
-    float* xs = reinterpret_cast<float*>(raw + (xs0 + w * 128 - tma::smem_u32(raw)));
-    const auto swap_at = [&](int v) { return reinterpret_cast<float*>(raw + (swap0 + v * kSwap - tma::smem_u32(raw))); };
-    uint32_t turn = 0, swaps = 0;
+    const bool gate = quad < 2;
+    // this warp's scales of x, and what it hands over and is handed
+    float* xs = reinterpret_cast<float*>(raw + (xs0 + w * kScaleBytes - tma::smem_u32(raw)));
+    float* mine = reinterpret_cast<float*>(raw + (swap0 + w * kSwap - tma::smem_u32(raw)));
+    const float* theirs = reinterpret_cast<const float*>(raw + (swap0 + other * kSwap - tma::smem_u32(raw)));
+    int buf = 0;
+    uint32_t buf_turn = 0, swap_turn = 0;
     bool ok = true;
-    for (int tile = first_tile; ok && tile < total; tile += pairs, ++turn) {
+    for (int tile = first_tile; ok && tile < total; tile += pairs) {
       const Tile t = tile_at<NT>(a, starts, tile);
-      const uint32_t buf = turn % kD;
       // the row of w that this lane holds, and its row in the output
       int row, channel;
       if (GATED) {
         channel = t.row_tile * kRows + static_cast<int>(cta) * (kRows / 2) + 32 * (quad & 1) + lane;
-        row = quad < 2 ? channel : half + channel;
+        row = gate ? channel : half + channel;
       } else {
         row = channel = t.row_tile * 2 * kRows + static_cast<int>(cta) * kRows + 32 * quad + lane;
       }
       const bool live = channel < out_rows;
       const float ws = live ? ld_coherent(a.p.w_scales + static_cast<int64_t>(t.expert) * a.p.rows + row) : 0.0f;
-      ok = __all_sync(kAll, wait(full_sum(buf), turn / kD & 1));
+      __syncwarp();
+      for (int i = 0, c = 32 * which + lane; c < t.width; ++i, c += 64)
+        xs[32 * i + lane] = c < t.tokens ? ld_coherent(a.p.x_scales + t.first + c) : 0.0f;
+      __syncwarp();
+      ok = __all_sync(kAll, wait(full_sum(buf), buf_turn));
       if (!ok) break;
       pair::fence_after();
-      for (int c = 32 * which; c < t.width; c += 64) {
+      if (32 * which >= t.width && lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));   // nothing here for it
+      for (int i = 0, c = 32 * which; c < t.width; ++i, c += 64) {
         uint32_t r[32];
         pair::ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * NT + c, r);
-        __syncwarp();
-        xs[lane] = c + lane < t.tokens ? ld_coherent(a.p.x_scales + t.first + c + lane) : 0.0f;
-        __syncwarp();
         pair::wait_ld();
+        if (c + 64 >= t.width) {               // the sums may be overwritten
+          pair::fence_before();
+          __syncwarp();
+          if (lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));
+        }
         float y[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]) * ws * xs[j];
-        const auto store = [&](int j, float v) {
-          if (live && c + j < t.tokens) {
-            const int64_t at = (t.first + c + j) * out_rows + channel;
-            if (a.p.out_f32)
-              static_cast<float*>(a.p.out)[at] = v;
-            else
-              static_cast<__nv_bfloat16*>(a.p.out)[at] = __float2bfloat16_rn(v);
-          }
-        };
+        for (int j = 0; j < 32; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(xs + 32 * i + j);
+          y[j] = __uint_as_float(r[j]) * ws * f.x;
+          y[j + 1] = __uint_as_float(r[j + 1]) * ws * f.y;
+          y[j + 2] = __uint_as_float(r[j + 2]) * ws * f.z;
+          y[j + 3] = __uint_as_float(r[j + 3]) * ws * f.w;
+        }
+        const int many = live ? t.tokens - c : 0;
+        const int64_t at = (t.first + c) * out_rows + channel;
         if constexpr (GATED) {
           // gate warps finish the first 16 tokens, up warps the last 16
-          float* mine = swap_at(w);
-          const float* theirs = swap_at(other);
-          const bool gate = quad < 2;
-          ok = __all_sync(kAll, wait(swap_done(w), (swaps & 1) ^ 1));
+          ok = __all_sync(kAll, wait(swap_done(w), swap_turn ^ 1));
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < 16; ++j) mine[32 * j + lane] = gate ? y[16 + j] : y[j];
           __syncwarp();
           if (lane == 0) tma::mbar_arrive(swap_ready(w));
-          ok = __all_sync(kAll, wait(swap_ready(other), swaps & 1));
+          ok = __all_sync(kAll, wait(swap_ready(other), swap_turn));
           if (!ok) break;
+          float h[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float v = theirs[32 * j + lane];
-            store(gate ? j : 16 + j, gate ? activate(a.p.act, y[j]) * v : activate(a.p.act, v) * y[16 + j]);
+            h[j] = activate(a.p.act, gate ? y[j] : v) * (gate ? v : y[16 + j]);
           }
           __syncwarp();
           if (lane == 0) tma::mbar_arrive(swap_done(other));
-          ++swaps;
+          swap_turn ^= 1;
+          store_column<16>(a.p, at + (gate ? 0 : 16 * static_cast<int64_t>(out_rows)), out_rows, gate ? many : many - 16, h);
         } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) store(j, y[j]);
+          store_column<32>(a.p, at, out_rows, many, y);
         }
       }
-      if (!ok) break;
-      pair::fence_before();
-      __syncwarp();
-      if (lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));
+      if (++buf == kD) buf = 0, buf_turn ^= 1;
     }
   }
   __syncwarp();
