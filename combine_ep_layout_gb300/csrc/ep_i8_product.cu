@@ -57,7 +57,7 @@ __host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : 4;
 __host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }         // sum buffers
 __host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
 __host__ __device__ constexpr int bytes_out(int nt) { return nt / 2 * kStep * 2; }
-constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over
+constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over, or 32 tokens of its output
 constexpr int kScaleBytes = 4 * 32 * 4;    // a writing warp's scales of x
 constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + 512;
 
@@ -71,39 +71,40 @@ struct Args {
 
 struct Tile {
   int expert, row_tile;
-  int64_t first;     // row of x
+  int first;         // row of x
   int tokens;        // rows of x that count
   int width;         // columns of the product: a multiple of 32
 };
 
 // Expert e's rows go to the fewest tiles, of (nearly) one size each.
-__device__ __forceinline__ int token_tiles(int64_t count, int nt) { return static_cast<int>((count + nt - 1) / nt); }
+__host__ __device__ __forceinline__ int token_tiles(int64_t count, int nt) { return static_cast<int>((count + nt - 1) / nt); }
 
+// A role's way through its pair's tiles, in ascending order.
 template <int NT>
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* starts, int tile) {
-  Tile t;
-  t.expert = 0;
-  if (a.p.first) {
-    int lo = 0, hi = a.p.experts;      // the last expert whose tiles begin at or before this one
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (starts[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid;
+struct Tiles {
+  const Args& a;
+  const int* starts;
+  int expert = 0;
+
+  __device__ __forceinline__ Tile operator()(int tile) {
+    Tile t;
+    int first = 0, count = static_cast<int>(a.p.n);
+    if (a.p.first) {
+      while (starts[expert + 1] <= tile) ++expert;
+      tile -= starts[expert];
+      first = ld_coherent(a.p.first + expert);
+      count = ld_coherent(a.p.count + expert);
     }
-    t.expert = lo;
-    tile -= starts[lo];
+    const unsigned tiles = token_tiles(count, NT), at = static_cast<unsigned>(tile) / static_cast<unsigned>(a.row_tiles);
+    const int per = static_cast<int>((count + tiles - 1) / tiles + 31) / 32 * 32;
+    t.expert = expert;
+    t.row_tile = tile - static_cast<int>(at) * a.row_tiles;
+    t.first = first + static_cast<int>(at) * per;
+    t.tokens = min(per, count - static_cast<int>(at) * per);
+    t.width = (t.tokens + 31) / 32 * 32;
+    return t;
   }
-  const int64_t count = a.p.first ? ld_coherent(a.p.count + t.expert) : a.p.n;
-  const int tiles = token_tiles(count, NT), at = tile / a.row_tiles;
-  const int per = static_cast<int>(((count + tiles - 1) / tiles + 31) / 32) * 32;
-  t.row_tile = tile % a.row_tiles;
-  t.first = (a.p.first ? ld_coherent(a.p.first + t.expert) : 0) + static_cast<int64_t>(at) * per;
-  t.tokens = static_cast<int>(min(static_cast<int64_t>(per), count - static_cast<int64_t>(at) * per));
-  t.width = (t.tokens + 31) / 32 * 32;
-  return t;
-}
+};
 
 // Waits of one CTA: false, and the CTA marked, when the limit has passed or the mark is there.
 struct Waits {
@@ -144,26 +145,65 @@ __device__ __forceinline__ void write16(uint32_t addr, uint32_t a, uint32_t b, u
 }
 
 // v sigmoid(s): silu with s = v; the tanh form of gelu is the same with
-// s = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh(u)) / 2 is sigmoid(2 u).
+// s = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh(u)) / 2 is sigmoid(2 u).  The exponential
+// is off by 2^-22 and by the rounding of its argument, |s| 2^-23, which sigmoid's slope takes
+// to under 4 2^-24 of |v|.
 __device__ __forceinline__ float activate(int act, float v) {
   const float s = act == EP_ACT_SILU ? v : v * fmaf(0.07135481282553f * v, v, 1.5957691216057308f);
-  return __fdividef(v, 1.0f + expf(-s));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * s));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return v * r;
 }
 
-// A lane's channel of the first `many` of N tokens.
+// A warp's 8 N tokens of 32 channels, as fragments: y[h][i][e] is channel 16 h + lane / 4 + 8 (e / 2) of
+// token 8 i + 2 (lane % 4) + e % 2.  `many` tokens and `channels` channels count.  bf16: turned by
+// stmatrix through 64 bytes a token at `stage`, and written as 16-byte pieces where the output's rows allow them.
 template <int N>
-__device__ __forceinline__ void store_column(const I8ProductParams& p, int64_t at, int pitch, int many, const float (&y)[N]) {
+__device__ __forceinline__ void store_tile(const I8ProductParams& p, bool wide, uint32_t stage, int lane, int64_t at, int pitch, int many,
+                                           int channels, const float (&y)[2][N][4]) {
   if (p.out_f32) {
     float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
-    for (int j = 0; j < N; ++j, out += pitch)
-      if (j < many) *out = y[j];
-  } else {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j, out += pitch)
-      if (j < many) *out = __float2bfloat16_rn(y[j]);
+      for (int e = 0; e < 2; ++e) {
+        const int token = 8 * i + 2 * (lane & 3) + e;
+        float* row = out + static_cast<int64_t>(token) * pitch + (lane >> 2);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (token < many && 8 * g + (lane >> 2) < channels) row[8 * g] = y[g >> 1][i][2 * (g & 1) + e];
+      }
+    return;
   }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+  // piece (8 channels) g of a token lies at place g ^ (token / 2 % 4): no two of a store on the same banks
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t v[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(y[g >> 1][i][2 * (g & 1)], y[g >> 1][i][2 * (g & 1) + 1]);
+      v[g] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    pair::store_transposed(stage + 64 * (8 * i + (lane & 7)) + 16 * ((lane >> 3) ^ ((lane >> 1) & 3)), v[0], v[1], v[2], v[3]);
+  }
+  __syncwarp();
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int token = 8 * i + lane / 4, piece = lane % 4;
+      const uint4 v = read16(stage + 64 * token + 16 * (piece ^ ((token >> 1) & 3)));
+      if (token < many && 8 * piece < channels) *reinterpret_cast<uint4*>(out + static_cast<int64_t>(token) * pitch + 8 * piece) = v;
+    }
+  } else if (lane < channels) {
+    for (int j = 0; j < 8 * N && j < many; ++j, out += pitch) {
+      uint16_t v;
+      asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(stage + 64 * j + 16 * ((lane >> 3) ^ ((j >> 1) & 3)) + 2 * (lane & 7)) : "memory");
+      out[lane] = __ushort_as_bfloat16(v);
+    }
+  }
+  __syncwarp();
 }
 
 template <int NT, bool GATED>
@@ -236,17 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   const Waits wait{&dead, a.p.wait_ns};
   const int pairs = static_cast<int>(gridDim.x) / 2, first_tile = static_cast<int>(blockIdx.x) / 2;
   const int half = a.p.rows / 2;
+  Tiles<NT> tile_of{a, starts};
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < total; tile += pairs) {
-        const Tile t = tile_at<NT>(a, starts, tile);
+        const Tile t = tile_of(tile);
         const int64_t row0 = static_cast<int64_t>(t.expert) * a.p.rows;
         const int lead = t.row_tile * (GATED ? kRows : 2 * kRows) + static_cast<int>(cta) * (GATED ? kRows / 2 : kRows);
         const int y0 = static_cast<int>(row0 + lead), y1 = GATED ? y0 + half : y0 + kRows / 2;
-        const int yx = static_cast<int>(t.first) + static_cast<int>(cta) * (t.width / 2);
+        const int yx = t.first + static_cast<int>(cta) * (t.width / 2);
         for (int k = 0; k < a.steps; ++k, ++it) {
           const uint32_t s = it % s1, at = base + s * kIn;
           if (!(ok = wait(empty_in(s), (it / s1 & 1) ^ 1))) break;
@@ -269,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       uint32_t stage_turn = 0, buf_turn = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < total; tile += pairs) {
-        const Tile t = tile_at<NT>(a, starts, tile);
+        const Tile t = tile_of(tile);
         const uint32_t d = tmem + buf * NT, shape = pair::shape_f16(t.width);
         if (!(ok = __all_sync(kAll, wait(empty_sum(buf), buf_turn ^ 1)))) break;
         pair::fence_after();
@@ -370,22 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
     // this warp's scales of x, and what it hands over and is handed
     float* xs = reinterpret_cast<float*>(raw + (xs0 + w * kScaleBytes - tma::smem_u32(raw)));
     float* mine = reinterpret_cast<float*>(raw + (swap0 + w * kSwap - tma::smem_u32(raw)));
+    const uint32_t stage = swap0 + w * kSwap;
+    const bool wide = out_rows % 8 == 0 && (reinterpret_cast<uintptr_t>(a.p.out) & 15) == 0;
     const float* theirs = reinterpret_cast<const float*>(raw + (swap0 + other * kSwap - tma::smem_u32(raw)));
     int buf = 0;
     uint32_t buf_turn = 0, swap_turn = 0;
     bool ok = true;
     for (int tile = first_tile; ok && tile < total; tile += pairs) {
-      const Tile t = tile_at<NT>(a, starts, tile);
-      // the row of w that this lane holds, and its row in the output
-      int row, channel;
-      if (GATED) {
-        channel = t.row_tile * kRows + static_cast<int>(cta) * (kRows / 2) + 32 * (quad & 1) + lane;
-        row = gate ? channel : half + channel;
-      } else {
-        row = channel = t.row_tile * 2 * kRows + static_cast<int>(cta) * kRows + 32 * quad + lane;
+      const Tile t = tile_of(tile);
+      // the warp's 32 output channels, their rows of w, and the scales of the four that a lane has
+      const int channel = GATED ? t.row_tile * kRows + static_cast<int>(cta) * (kRows / 2) + 32 * (quad & 1)
+                                : t.row_tile * 2 * kRows + static_cast<int>(cta) * kRows + 32 * quad;
+      const int channels = out_rows - channel, row = GATED && !gate ? half + channel : channel;
+      float ws[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int at = 8 * g + (lane >> 2);
+        ws[g] = at < channels ? ld_coherent(a.p.w_scales + static_cast<int64_t>(t.expert) * a.p.rows + row + at) : 0.0f;
       }
-      const bool live = channel < out_rows;
-      const float ws = live ? ld_coherent(a.p.w_scales + static_cast<int64_t>(t.expert) * a.p.rows + row) : 0.0f;
       __syncwarp();
       for (int i = 0, c = 32 * which + lane; c < t.width; ++i, c += 64)
         xs[32 * i + lane] = c < t.tokens ? ld_coherent(a.p.x_scales + t.first + c) : 0.0f;
@@ -395,47 +438,51 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       pair::fence_after();
       if (32 * which >= t.width && lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));   // nothing here for it
       for (int i = 0, c = 32 * which; c < t.width; ++i, c += 64) {
-        uint32_t r[32];
-        pair::ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * NT + c, r);
+        uint32_t r[2][16];
+        const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * NT + c;
+        pair::ld16x32(from, r[0]);
+        pair::ld16x32(from + (16u << 16), r[1]);
         pair::wait_ld();
         if (c + 64 >= t.width) {               // the sums may be overwritten
           pair::fence_before();
           __syncwarp();
           if (lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));
         }
-        float y[32];
+        float y[2][4][4];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(xs + 32 * i + j);
-          y[j] = __uint_as_float(r[j]) * ws * f.x;
-          y[j + 1] = __uint_as_float(r[j + 1]) * ws * f.y;
-          y[j + 2] = __uint_as_float(r[j + 2]) * ws * f.z;
-          y[j + 3] = __uint_as_float(r[j + 3]) * ws * f.w;
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(xs + 32 * i + 8 * j + 2 * (lane & 3));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[h][j][e] = __uint_as_float(r[h][4 * j + e]) * ws[2 * h + e / 2] * (e & 1 ? f.y : f.x);
         }
-        const int many = live ? t.tokens - c : 0;
-        const int64_t at = (t.first + c) * out_rows + channel;
+        const int many = t.tokens - c;
+        const int64_t at = static_cast<int64_t>(t.first + c) * out_rows + channel;
         if constexpr (GATED) {
           // gate warps finish the first 16 tokens, up warps the last 16
-          ok = __all_sync(kAll, wait(swap_done(w), swap_turn ^ 1));
-          if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mine[32 * j + lane] = gate ? y[16 + j] : y[j];
+          for (int j = 0; j < 16; ++j) mine[32 * j + lane] = gate ? y[j >> 3][2 + (j >> 2 & 1)][j & 3] : y[j >> 3][j >> 2 & 1][j & 3];
           __syncwarp();
           if (lane == 0) tma::mbar_arrive(swap_ready(w));
           ok = __all_sync(kAll, wait(swap_ready(other), swap_turn));
           if (!ok) break;
-          float h[16];
+          float h[2][2][4];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float v = theirs[32 * j + lane];
-            h[j] = activate(a.p.act, gate ? y[j] : v) * (gate ? v : y[16 + j]);
+            const float v = theirs[32 * j + lane], own = gate ? y[j >> 3][j >> 2 & 1][j & 3] : y[j >> 3][2 + (j >> 2 & 1)][j & 3];
+            h[j >> 3][j >> 2 & 1][j & 3] = activate(a.p.act, gate ? own : v) * (gate ? v : own);
           }
           __syncwarp();
           if (lane == 0) tma::mbar_arrive(swap_done(other));
+          // what was handed over has been read: its place takes the output on its way
+          ok = __all_sync(kAll, wait(swap_done(w), swap_turn));
+          if (!ok) break;
           swap_turn ^= 1;
-          store_column<16>(a.p, at + (gate ? 0 : 16 * static_cast<int64_t>(out_rows)), out_rows, gate ? many : many - 16, h);
+          store_tile<2>(a.p, wide, stage, lane, at + (gate ? 0 : 16 * static_cast<int64_t>(out_rows)), out_rows,
+                         gate ? many : many - 16, channels, h);
         } else {
-          store_column<32>(a.p, at, out_rows, many, y);
+          store_tile<4>(a.p, wide, stage, lane, at, out_rows, many, channels, y);
         }
       }
       if (++buf == kD) buf = 0, buf_turn ^= 1;
