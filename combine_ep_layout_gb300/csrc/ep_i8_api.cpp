@@ -155,8 +155,9 @@ int ep_i8_grouped(ep_handle_t h, const int8_t* x, const float* x_scales, const i
                                      out, out_dtype, &p);
         rc != EP_OK)
       return rc;
-    if (static_cast<int64_t>(r.experts) * rows > INT32_MAX)
-      return fail(EP_EINVAL, "experts * rows must be below 2^31");
+    // row numbers of tiles that reach past the end are 32 bits
+    if (static_cast<int64_t>(r.experts) * rows > INT32_MAX - 4096 || r.rcap > INT32_MAX - 4096)
+      return fail(EP_EINVAL, "experts * rows and the receive capacity must be below 2^31 - 4096");
     p.first = r.first;
     p.count = r.count;
     p.experts = r.experts;

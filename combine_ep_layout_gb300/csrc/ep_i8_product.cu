@@ -20,8 +20,9 @@
 //           32 rows, and an eighth of x
 //   20-27   sums times scales, activation, output; up to 128 tokens the sums are double
 //           buffered, so that this runs beside the next tile
-// Gated: 64 gate rows and their 64 up rows make a CTA's 128; the warps that hold them
-// swap halves through shared memory.
+// A CTA's rows are two half tiles of up to 64, in the lanes from 0 and from 64 on: gated, the
+// second half is the up rows of the first, and the warps that hold them swap halves through
+// shared memory.  Where rows are few, half tiles are smaller, so that every SM has some.
 //
 // Every wait is bounded.  A warp that gives up records it, marks its CTA and leaves; the
 // others of the pair give up by the mark or by their own limit, and all meet before the
@@ -31,6 +32,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <climits>
 #include <cstdint>
 
 #include "ep_gb300_i8.h"
@@ -64,6 +67,7 @@ constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + 512;
 struct Args {
   I8ProductParams p;
   int steps;         // stages of a tile
+  int part;          // weight rows of a CTA's half tile: a multiple of 8 up to 64
   int row_tiles;     // pair tiles along the weight rows
   int stages_in;
   CUtensorMap w, x;
@@ -280,18 +284,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
 
   if (warp == 0) {
     if (lane == 0) {
+      const uint32_t bytes = 2 * a.part * kStep + kTok * kStep;
       uint32_t it = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < total; tile += pairs) {
         const Tile t = tile_of(tile);
-        const int64_t row0 = static_cast<int64_t>(t.expert) * a.p.rows;
-        const int lead = t.row_tile * (GATED ? kRows : 2 * kRows) + static_cast<int>(cta) * (GATED ? kRows / 2 : kRows);
-        const int y0 = static_cast<int>(row0 + lead), y1 = GATED ? y0 + half : y0 + kRows / 2;
+        const int lead = (2 * t.row_tile + static_cast<int>(cta)) * (GATED ? a.part : 2 * a.part);
+        const int y0 = t.expert * a.p.rows + lead, y1 = y0 + (GATED ? half : a.part);
         const int yx = t.first + static_cast<int>(cta) * (t.width / 2);
         for (int k = 0; k < a.steps; ++k, ++it) {
           const uint32_t s = it % s1, at = base + s * kIn;
           if (!(ok = wait(empty_in(s), (it / s1 & 1) ^ 1))) break;
-          tma::mbar_expect_tx(full_in(s), kIn);
+          tma::mbar_expect_tx(full_in(s), bytes);
           pair::load_box(at, &a.w, k * kStep, y0, full_in(s));
           pair::load_box(at + kRows / 2 * kStep, &a.w, k * kStep, y1, full_in(s));
           pair::load_box(at + kRows * kStep, &a.x, k * kStep, yx, full_in(s));
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
     const int w = (warp - 4) % kWideners, group = (warp - 4) / kWideners, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
     const int thread = 32 * w + lane, xrow = thread % kTok, xpart = thread / kTok;
     constexpr int kParts = 256 / kTok, kMine = kParts < 8 ? 8 / kParts : 1;   // threads of a row of x, its chunks of a thread
-    const bool has_x = xpart < 8;
+    const bool has_x = xpart < 8, has_rows = a.part > 32 * (quad & 1);
     const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * (kColumnsA / 2);
     const uint32_t from_a = base + row * kStep, from_x = base + kRows * kStep + xrow * kStep;
     const uint32_t to_x = out0 + xrow * 128;
@@ -359,11 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       if (!ok) break;
       pair::fence_after();
       uint4 va[4], vx[kMine];
+      if (has_rows)
 #pragma unroll
       for (int c = 0; c < 4; ++c) va[c] = read16(from_a + in * kIn + (((4 * part + c) ^ (row & 7)) << 4));
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
         if (has_x) vx[i] = read16(from_x + in * kIn + (((xpart + i * kParts) ^ (xrow & 7)) << 4));
+      if (has_rows)
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
         uint32_t r[16];
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   } else if (warp >= kFirstWriter) {
     const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;
     const int out_rows = GATED ? half : a.p.rows;
-    const bool gate = quad < 2;
+    const bool gate = quad < 2;                // (not gated: the first half tile)
     // this warp's scales of x, and what it hands over and is handed
     float* xs = reinterpret_cast<float*>(raw + (xs0 + w * kScaleBytes - tma::smem_u32(raw)));
     float* mine = reinterpret_cast<float*>(raw + (swap0 + w * kSwap - tma::smem_u32(raw)));
@@ -420,9 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
     for (int tile = first_tile; ok && tile < total; tile += pairs) {
       const Tile t = tile_of(tile);
       // the warp's 32 output channels, their rows of w, and the scales of the four that a lane has
-      const int channel = GATED ? t.row_tile * kRows + static_cast<int>(cta) * (kRows / 2) + 32 * (quad & 1)
-                                : t.row_tile * 2 * kRows + static_cast<int>(cta) * kRows + 32 * quad;
-      const int channels = out_rows - channel, row = GATED && !gate ? half + channel : channel;
+      const int lead = (2 * t.row_tile + static_cast<int>(cta)) * (GATED ? a.part : 2 * a.part) + (GATED || gate ? 0 : a.part);
+      const int channel = lead + 32 * (quad & 1), row = GATED && !gate ? half + channel : channel;
+      const int channels = min(out_rows - channel, a.part - 32 * (quad & 1));
       float ws[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -525,19 +531,40 @@ cudaError_t map_of(CUtensorMap* map, const void* at, int64_t rows, int cols, int
              : cudaErrorInvalidValue;
 }
 
+struct Gpu {
+  int device, sms;
+};
+cudaError_t current_gpu(Gpu* g) {
+  static std::atomic<int> known[64];   // SMs by device, 0: not asked yet
+  if (const cudaError_t e = cudaGetDevice(&g->device); e != cudaSuccess) return e;
+  g->sms = g->device < 64 ? known[g->device].load(std::memory_order_relaxed) : 0;
+  if (g->sms == 0) {
+    if (const cudaError_t e = cudaDeviceGetAttribute(&g->sms, cudaDevAttrMultiProcessorCount, g->device); e != cudaSuccess) return e;
+    if (g->device < 64) known[g->device].store(g->sms, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
 template <int NT, bool GATED>
-cudaError_t launch(Args& a, int num_sms, int64_t most_tiles, cudaStream_t s) {
+cudaError_t launch(Args& a, const Gpu& gpu, int64_t most_tiles, cudaStream_t s) {
   const int starts = a.p.first ? 4 * (a.p.experts + 1) : 0;
   const int room = kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - starts;
   a.stages_in = std::min(16, room / bytes_in(NT));
   static_assert((kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - 4 * 2049) / bytes_in(NT) >= stages_out(NT));
   const int smem = 1024 + a.stages_in * bytes_in(NT) + stages_out(NT) * bytes_out(NT) + kFixed + starts;
   if (const cudaError_t e = map_of(&a.x, a.p.x, a.p.n, a.p.cols, NT / 2); e != cudaSuccess) return e;
-  if (const cudaError_t e = cudaFuncSetAttribute(i8_mma_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      e != cudaSuccess)
-    return e;
+  if (const cudaError_t e = map_of(&a.w, a.p.w, static_cast<int64_t>(a.p.experts) * a.p.rows, a.p.cols, a.part); e != cudaSuccess) return e;
+  // the kernel's shared-memory limit is raised once on each device
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << (gpu.device & 63);
+  if (gpu.device >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
+    if (const cudaError_t e = cudaFuncSetAttribute(i8_mma_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared + 1024);
+        e != cudaSuccess)
+      return e;
+    if (gpu.device < 64) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(num_sms / 2, most_tiles)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(gpu.sms / 2, most_tiles)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -550,35 +577,64 @@ cudaError_t launch(Args& a, int num_sms, int64_t most_tiles, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, i8_mma_kernel<NT, GATED>, a);
 }
 
+// Cycles of a tile: a stage takes the longest of its products (measured, 8 instructions), widening
+// and its share of the memory's rate; the ends are set-up and output, which up to
+// 128 tokens run beside the next tile.
+int64_t tile_cost(int width, int part, int steps) {
+  const int products = 8 * (9 + width / 2), widen = 330 + 3 * width / 2, bytes = 2 * part * kStep / 22;
+  return static_cast<int64_t>(steps) * std::max(products, std::max(widen, bytes)) + (width > 128 ? 6000 : 2000);
+}
+
+// Tokens of a tile and weight rows of a half tile of a dense product: what takes the fewest cycles
+// when each pair of SMs takes its share of the tiles in turn.
+void choose(int64_t n, int channels, bool gated, int steps, int pairs, int* nt, int* part) {
+  int64_t least = INT64_MAX;
+  const int per = gated ? 2 : 4;             // channels of a pair tile for each row of a half tile
+  for (int t = 32; t <= 256; t *= 2) {
+    const int64_t token_tiles = (n + t - 1) / t;
+    const int width = static_cast<int>(((n + token_tiles - 1) / token_tiles + 31) / 32) * 32;
+    for (int m = 8; m <= 64; m += 8) {
+      const int64_t tiles = token_tiles * ((channels + per * m - 1) / (per * m));
+      const int64_t cost = (tiles + pairs - 1) / pairs * tile_cost(width, m, steps);
+      if (cost < least) least = cost, *nt = t, *part = m;
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t LaunchI8Product(const I8ProductParams& p, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
-  int dev = 0, sms = 0;
-  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-  if (const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev); e != cudaSuccess) return e;
+  Gpu gpu;
+  if (const cudaError_t e = current_gpu(&gpu); e != cudaSuccess) return e;
   const bool gated = p.act != EP_ACT_NONE;
+  const int channels = gated ? p.rows / 2 : p.rows;
   Args a{};
   a.p = p;
   a.steps = (p.cols + kStep - 1) / kStep;
-  a.row_tiles = gated ? (p.rows / 2 + kRows - 1) / kRows : (p.rows + 2 * kRows - 1) / (2 * kRows);
-  if (const cudaError_t e = map_of(&a.w, p.w, static_cast<int64_t>(p.experts) * p.rows, p.cols, kRows / 2); e != cudaSuccess)
-    return e;
-  // the tile's tokens: the average expert's rows, and some more, in as few tiles as that allows
-  const int64_t mean = p.first ? p.entries / p.experts + 1 : p.n;
-  const int nt = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : 256;
+  int nt = 256;
+  a.part = kRows / 2;
+  if (!p.first) {
+    choose(p.n, channels, gated, a.steps, gpu.sms / 2, &nt, &a.part);
+  } else {
+    // the average expert's rows, and some more, in one tile
+    const int64_t mean = p.entries / p.experts + 1;
+    nt = mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : 256;
+  }
+  const int per = gated ? 2 * a.part : 4 * a.part;
+  a.row_tiles = (channels + per - 1) / per;
   const int64_t most = static_cast<int64_t>(a.row_tiles) * (p.first ? std::min<int64_t>(p.entries, p.experts + p.entries / nt)
                                                                     : (p.n + nt - 1) / nt);
   if (gated) {
-    if (nt == 32) return launch<32, true>(a, sms, most, s);
-    if (nt == 64) return launch<64, true>(a, sms, most, s);
-    if (nt == 128) return launch<128, true>(a, sms, most, s);
-    return launch<256, true>(a, sms, most, s);
+    if (nt == 32) return launch<32, true>(a, gpu, most, s);
+    if (nt == 64) return launch<64, true>(a, gpu, most, s);
+    if (nt == 128) return launch<128, true>(a, gpu, most, s);
+    return launch<256, true>(a, gpu, most, s);
   }
-  if (nt == 32) return launch<32, false>(a, sms, most, s);
-  if (nt == 64) return launch<64, false>(a, sms, most, s);
-  if (nt == 128) return launch<128, false>(a, sms, most, s);
-  return launch<256, false>(a, sms, most, s);
+  if (nt == 32) return launch<32, false>(a, gpu, most, s);
+  if (nt == 64) return launch<64, false>(a, gpu, most, s);
+  if (nt == 128) return launch<128, false>(a, gpu, most, s);
+  return launch<256, false>(a, gpu, most, s);
 }
 
 cudaError_t ReadI8Error(int32_t* value, cudaStream_t s) {

@@ -70,7 +70,7 @@ int ep_i8_linear(const int8_t *x, const float *x_scales, int32_t num_tokens, con
  *   out[s] = ep_i8_linear of x[s] with w[e] and w_scales[e].
  * x: int8 [Rcap, cols], x_scales: fp32 [Rcap]; w: int8 [E, rows, cols]; w_scales:
  * fp32 [E, rows]; out [Rcap, rows] (gated: [Rcap, rows / 2]).  cols and rows
- * need not be the handle's hidden_dim; E * rows is below 2^31.  Padding rows are left as they are, and what x
+ * need not be the handle's hidden_dim; E * rows and Rcap are below 2^31 - 4096.  Padding rows are left as they are, and what x
  * holds there does not matter. */
 int ep_i8_grouped(ep_handle_t h, const int8_t *x, const float *x_scales, const int8_t *w,
                   const float *w_scales, int32_t rows, int32_t cols, int32_t activation,
