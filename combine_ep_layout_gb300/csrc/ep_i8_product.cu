@@ -15,9 +15,8 @@
 //   0       TMA loads of both operands, a ring of 128 columns a stage
 //   1       (first CTA) issues the products
 //   2       tensor memory
-//   4-19    widen, 8 warps a stage and the two eights in turn, as a stage's latency (reads, fence,
-//           tensor memory, barriers) is twice its work: half of a stage's weight columns for
-//           32 rows, and an eighth of x
+//   4-19    widen, in groups that take the stages in turn, as a stage's latency (reads, fence,
+//           tensor memory, barriers) is a multiple of its work: 32 weight rows a warp, and a share of x
 //   20-27   sums times scales, activation, output; up to 128 tokens the sums are double
 //           buffered, so that this runs beside the next tile
 // A CTA's rows are two half tiles of up to 64, in the lanes from 0 and from 64 on: gated, the
@@ -48,21 +47,26 @@ namespace {
 __device__ int32_t g_error;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWideners = 8, kGroups = 2, kWriters = 8;   // warps of a stage, groups of them; writing warps
-constexpr int kFirstWriter = 4 + kWideners * kGroups, kThreads = 32 * (kFirstWriter + kWriters);
+constexpr int kWideners = 16, kWriters = 8;   // warps
+constexpr int kFirstWriter = 4 + kWideners, kThreads = 32 * (kFirstWriter + kWriters);
 constexpr int kRows = 128;                 // weight rows of a CTA
 constexpr int kStep = 128;                 // columns of a stage
 constexpr int kColumnsA = kStep / 2;       // tensor memory columns of a stage's weights
 constexpr uint32_t kTmem = 512;
 constexpr int kMaxShared = 232448 - 1024 - 64;   // less what aligning the buffers may take, and static data
 
-__host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : 4; }   // widened stages
+// Groups of widening warps that take the stages in turn, and widened stages: as many as tensor memory
+// holds beside the sums, up to 6.  Up to 64 tokens a stage's latency is what counts (4 groups; with 2
+// 16 tokens x 2048 x 7168 took 27 us).
+__host__ __device__ constexpr int groups(int nt) { return nt <= 64 ? 4 : 2; }
+__host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : nt == 128 ? 4 : 6; }
 __host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }         // sum buffers
 __host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
 __host__ __device__ constexpr int bytes_out(int nt) { return nt / 2 * kStep * 2; }
 constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over, or 32 tokens of its output
+constexpr int kBarBytes = 528;
 constexpr int kScaleBytes = 4 * 32 * 4;    // a writing warp's scales of x
-constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + 512;
+constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + kBarBytes;
 
 struct Args {
   I8ProductParams p;
@@ -213,6 +217,8 @@ __device__ __forceinline__ void store_tile(const I8ProductParams& p, bool wide, 
 template <int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_kernel(const __grid_constant__ Args a) {
   constexpr int kTok = NT / 2, kIn = bytes_in(NT), kOut = bytes_out(NT), kS2 = stages_out(NT), kD = sums(NT);
+  constexpr int kGroups = groups(NT), kOfStage = kWideners / kGroups;      // warps of a stage
+  static_assert(kS2 >= kGroups && kD * NT + kS2 * kColumnsA <= static_cast<int>(kTmem));
   constexpr uint32_t kSumColumns = kD * NT;
   extern __shared__ uint8_t raw[];
   __shared__ int dead;
@@ -221,23 +227,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   const uint32_t cta = pair::rank();
   const uint32_t base = (tma::smem_u32(raw) + 1023) & ~1023u;
   const uint32_t out0 = base + s1 * kIn, swap0 = out0 + kS2 * kOut, xs0 = swap0 + kWriters * kSwap, bars = xs0 + kWriters * kScaleBytes;
-  int* starts = reinterpret_cast<int*>(raw + (bars + 512 - tma::smem_u32(raw)));
+  int* starts = reinterpret_cast<int*>(raw + (bars + kBarBytes - tma::smem_u32(raw)));
   // barriers: s1 (at most 16) full, empty of the int8 ring; kS2 full, empty of the widened one; sums
   // full, empty; swaps ready, done; end
   const auto full_in = [&](int s) { return bars + 8 * s; };
   const auto empty_in = [&](int s) { return bars + 128 + 8 * s; };
   const auto full_out = [&](int s) { return bars + 256 + 8 * s; };
-  const auto empty_out = [&](int s) { return bars + 288 + 8 * s; };
-  const auto full_sum = [&](int s) { return bars + 320 + 8 * s; };
-  const auto empty_sum = [&](int s) { return bars + 336 + 8 * s; };
-  const auto swap_ready = [&](int s) { return bars + 352 + 8 * s; };
-  const auto swap_done = [&](int s) { return bars + 416 + 8 * s; };
-  const uint32_t end_bar = bars + 480;
+  const auto empty_out = [&](int s) { return bars + 304 + 8 * s; };
+  const auto full_sum = [&](int s) { return bars + 352 + 8 * s; };
+  const auto empty_sum = [&](int s) { return bars + 368 + 8 * s; };
+  const auto swap_ready = [&](int s) { return bars + 384 + 8 * s; };
+  const auto swap_done = [&](int s) { return bars + 448 + 8 * s; };
+  const uint32_t end_bar = bars + 512;
 
   if (threadIdx.x == 0) {
     dead = 0;
-    for (int s = 0; s < s1; ++s) tma::mbar_init(full_in(s), 1), tma::mbar_init(empty_in(s), kWideners);
-    for (int s = 0; s < kS2; ++s) tma::mbar_init(full_out(s), 2 * kWideners), tma::mbar_init(empty_out(s), 1);
+    for (int s = 0; s < s1; ++s) tma::mbar_init(full_in(s), 1), tma::mbar_init(empty_in(s), kOfStage);
+    for (int s = 0; s < kS2; ++s) tma::mbar_init(full_out(s), 2 * kOfStage), tma::mbar_init(empty_out(s), 1);
     for (int s = 0; s < kD; ++s) tma::mbar_init(full_sum(s), 1), tma::mbar_init(empty_sum(s), 2 * kWriters);
     for (int s = 0; s < kWriters; ++s) tma::mbar_init(swap_ready(s), 1), tma::mbar_init(swap_done(s), 1);
     tma::mbar_init(end_bar, 1);
@@ -283,27 +289,35 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   Tiles<NT> tile_of{a, starts};
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t bytes = 2 * a.part * kStep + kTok * kStep;
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = first_tile; ok && tile < total; tile += pairs) {
-        const Tile t = tile_of(tile);
-        const int lead = (2 * t.row_tile + static_cast<int>(cta)) * (GATED ? a.part : 2 * a.part);
-        const int y0 = t.expert * a.p.rows + lead, y1 = y0 + (GATED ? half : a.part);
-        const int yx = t.first + static_cast<int>(cta) * (t.width / 2);
-        for (int k = 0; k < a.steps; ++k, ++it) {
-          const uint32_t s = it % s1, at = base + s * kIn;
-          if (!(ok = wait(empty_in(s), (it / s1 & 1) ^ 1))) break;
-          tma::mbar_expect_tx(full_in(s), bytes);
-          pair::load_box(at, &a.w, k * kStep, y0, full_in(s));
-          pair::load_box(at + kRows / 2 * kStep, &a.w, k * kStep, y1, full_in(s));
-          pair::load_box(at + kRows * kStep, &a.x, k * kStep, yx, full_in(s));
+    // as for the products, the whole warp goes along and one elected lane issues
+    const bool one = pair::elect();
+    const uint32_t bytes = 2 * a.part * kStep + kTok * kStep;
+    int in = 0;
+    uint32_t turn = 0, copies = 0;
+    bool ok = true;
+    for (int tile = first_tile; ok && tile < total; tile += pairs) {
+      const Tile t = tile_of(tile);
+      const int lead = (2 * t.row_tile + static_cast<int>(cta)) * (GATED ? a.part : 2 * a.part);
+      const int y0 = t.expert * a.p.rows + lead, y1 = y0 + (GATED ? half : a.part);
+      const int yx = t.first + static_cast<int>(cta) * (t.width / 2);
+      for (int k = 0; k < a.steps; ++k) {
+        if (!(ok = __all_sync(kAll, wait(empty_in(in), turn ^ 1)))) break;
+        if (one) {
+          const uint32_t at = base + in * kIn, bar = full_in(in);
+          tma::mbar_expect_tx(bar, bytes);
+          pair::load_box(at, &a.w, k * kStep, y0, bar);
+          pair::load_box(at + kRows / 2 * kStep, &a.w, k * kStep, y1, bar);
+          pair::load_box(at + kRows * kStep, &a.x, k * kStep, yx, bar);
         }
+        __syncwarp();
+        copies = min(copies + 1, static_cast<uint32_t>(s1));
+        if (++in == s1) in = 0, turn ^= 1;
       }
-      // the copies in flight land before the block ends
-      for (uint32_t j = it > static_cast<uint32_t>(s1) ? it - s1 : 0; j < it; ++j)
-        tma::mbar_wait_bounded(full_in(j % s1), j / s1 & 1, tma::kDrainNs);
+    }
+    // the copies in flight land before the block ends
+    for (; copies != 0; --copies) {
+      if (--in < 0) in = s1 - 1, turn ^= 1;
+      tma::mbar_wait_bounded(full_in(in), turn, tma::kDrainNs);
     }
   } else if (warp == 1) {
     if (cta == 0) {
@@ -343,11 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
     }
   } else if (warp >= 4 && warp < kFirstWriter) {
-    const int w = (warp - 4) % kWideners, group = (warp - 4) / kWideners, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
+    const int w = (warp - 4) % kOfStage, group = (warp - 4) / kOfStage, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
+    constexpr int kMineA = 32 / kOfStage;      // 16-column chunks of a row of w that a thread widens
+    constexpr int kRowParts = 32 * kOfStage / kTok, kMine = kRowParts < 8 ? 8 / kRowParts : 1;   // threads of a row of x, its chunks of a thread
     const int thread = 32 * w + lane, xrow = thread % kTok, xpart = thread / kTok;
-    constexpr int kParts = 256 / kTok, kMine = kParts < 8 ? 8 / kParts : 1;   // threads of a row of x, its chunks of a thread
     const bool has_x = xpart < 8, has_rows = a.part > 32 * (quad & 1);
-    const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * (kColumnsA / 2);
+    const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * 8 * kMineA;
     const uint32_t from_a = base + row * kStep, from_x = base + kRows * kStep + xrow * kStep;
     const uint32_t to_x = out0 + xrow * 128;
     // the group's stage of either ring, and the parity of its turn there
@@ -362,16 +377,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       ok = __all_sync(kAll, wait(empty_out(out), out_turn ^ 1) && wait(full_in(in), in_turn));
       if (!ok) break;
       pair::fence_after();
-      uint4 va[4], vx[kMine];
+      uint4 va[kMineA], vx[kMine];
       if (has_rows)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) va[c] = read16(from_a + in * kIn + (((4 * part + c) ^ (row & 7)) << 4));
+      for (int c = 0; c < kMineA; ++c) va[c] = read16(from_a + in * kIn + (((kMineA * part + c) ^ (row & 7)) << 4));
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
-        if (has_x) vx[i] = read16(from_x + in * kIn + (((xpart + i * kParts) ^ (xrow & 7)) << 4));
+        if (has_x) vx[i] = read16(from_x + in * kIn + (((xpart + i * kRowParts) ^ (xrow & 7)) << 4));
       if (has_rows)
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
+      for (int c = 0; c < kMineA; c += 2) {
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
         if (has_x) {
-          const int c = xpart + i * kParts, c2 = 2 * (c & 3);
+          const int c = xpart + i * kRowParts, c2 = 2 * (c & 3);
           uint32_t q[8];
           widen(vx[i].x, q[0], q[1]);
           widen(vx[i].y, q[2], q[3]);
