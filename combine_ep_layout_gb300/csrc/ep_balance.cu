@@ -1,18 +1,24 @@
 // ep_balance.cu -- the router's training losses and their gradient
 // (include/ep_gb300_balance.h states the formulas).
 //
-// Bound by reading the scores once; a score costs one exp (sigmoid: two).
+// Bound by reading the scores once, as long as enough rows are under way; a score costs one
+// exp (sigmoid: two).
 //
 // Forward, two launches: each block of the first takes a run of consecutive
-// tokens, a warp a token at a time, and keeps a column of sums in every lane; for each
+// tokens, a warp two tokens at a time (the next two under way), and keeps a column of sums in every lane; for each
 // sequence that its run touches it writes one row of sums (probabilities, counts,
 // live tokens, squared lse).  The second adds those rows, 32 experts a block, and the last of its
-// blocks adds the losses.  The pairs (block, sequence) with tokens form a staircase, so
-// block + sequence numbers their rows.  Every sum has a fixed order; only whole numbers go
-// through atomics.
+// blocks adds the losses.  Few tokens of one sequence: one block does both.  The
+// pairs (block, sequence) with tokens form a staircase, so block + sequence numbers their
+// rows.  Every sum has a fixed order; only whole numbers go through atomics.
+//
+// Backward: a warp takes up to 8 consecutive tokens, two at a time and the next two under way, with the counts of their
+// sequence in registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "ep_balance_kernels.hpp"
@@ -27,7 +33,11 @@ namespace {
 using namespace route;
 using namespace rows;
 
-constexpr int kWarps = 8;
+constexpr int kFinalWarps = 16, kBackWarps = 8;
+// Warps of a block of sums: registers allow 32 of them up to 256 experts.  Two rows at a time up to
+// there, one beyond.
+__host__ __device__ constexpr int sum_warps(int v) { return v <= 8 ? 32 : v == 16 ? 16 : 8; }
+__host__ __device__ constexpr int at_once(int v) { return v <= 8 ? 2 : 1; }
 
 // A lane's scores of a row.  VEC: V consecutive ones; else every 32nd, which rows that are not
 // 16-byte aligned are read by in whole sectors.
@@ -49,60 +59,182 @@ __device__ __forceinline__ void load_scores(const T* row, int experts, int lane,
   }
 }
 
-// z becomes p; returns lse, -inf where every score is masked.  SIGMOID: soft gets exp(z - peak),
-// not_s gets 1 - sigmoid(z).
-template <int V, bool SIGMOID, bool GRAD>
-__device__ __forceinline__ float probabilities(float (&z)[V], float (&soft)[V], float (&not_s)[V]) {
-  const float peak = warp_max(lane_max(z));
-  float whole = 0.0f, part = 0.0f;
+// exp(x), x <= 0 or a finite sigmoid's argument: off by 2^-22 and the rounding of x log2(e).
+__device__ __forceinline__ float exp_fast(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float below(float z, float peak) {
+  return z > -INFINITY ? (z == peak ? 1.0f : exp_fast(z - peak)) : 0.0f;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// U rows: z becomes p; lse is -inf where every score is masked.  SIGMOID and GRAD: soft gets
+// exp(z - lse), not_s 1 - sigmoid(z).
+template <int U, int V, bool SIGMOID, bool GRAD>
+__device__ __forceinline__ void probabilities(float (&z)[U][V], float (&soft)[U][V], float (&not_s)[U][V], float (&lse)[U]) {
+  float peak[U], whole[U], part[U];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float e = exp_below(z[v], peak);
-    whole += e;
-    if constexpr (SIGMOID) {
-      // scaled by exp(-peak) where every score is below zero, so that ratios survive
-      const float t = expf(-fabsf(z[v])), inv = 1.0f / (1.0f + t);
-      const float s = peak < 0.0f ? e * inv : z[v] >= 0.0f ? inv : t * inv;
-      if constexpr (GRAD) soft[v] = e, not_s[v] = z[v] >= 0.0f ? t * inv : inv;
-      z[v] = z[v] > -INFINITY ? s : 0.0f;
-      part += z[v];
-    } else {
-      z[v] = e;
+  for (int u = 0; u < U; ++u) peak[u] = warp_max(lane_max(z[u]));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    whole[u] = part[u] = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float x = z[u][v], e = below(x, peak[u]);
+      whole[u] += e;
+      if constexpr (SIGMOID) {
+        // scaled by exp(-peak) where every score is below zero, so that ratios survive
+        const float t = exp_fast(-fabsf(x)), inv = reciprocal(1.0f + t);
+        const float s = peak[u] < 0.0f ? e * inv : x >= 0.0f ? inv : t * inv;
+        if constexpr (GRAD) soft[u][v] = e, not_s[u][v] = x >= 0.0f ? t * inv : inv;
+        z[u][v] = x > -INFINITY ? s : 0.0f;
+        part[u] += z[u][v];
+      } else {
+        z[u][v] = e;
+      }
     }
   }
-  whole = warp_sum(whole);
-  if constexpr (SIGMOID) part = warp_sum(part);
-  const float inv = whole > 0.0f ? 1.0f / whole : 0.0f;
-  const float inv_p = SIGMOID ? (part > 0.0f ? 1.0f / part : 0.0f) : inv;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    z[v] *= inv_p;
-    if constexpr (SIGMOID && GRAD) soft[v] *= inv;
+  for (int d = 16; d; d >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      whole[u] += __shfl_xor_sync(kAll, whole[u], d);
+      if constexpr (SIGMOID) part[u] += __shfl_xor_sync(kAll, part[u], d);
+    }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float inv = whole[u] > 0.0f ? 1.0f / whole[u] : 0.0f;
+    const float inv_p = SIGMOID ? (part[u] > 0.0f ? 1.0f / part[u] : 0.0f) : inv;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      z[u][v] *= inv_p;
+      if constexpr (SIGMOID && GRAD) soft[u][v] *= inv;
+    }
+    lse[u] = whole[u] > 0.0f ? peak[u] + logf(whole[u]) : -INFINITY;
   }
-  return whole > 0.0f ? peak + logf(whole) : -INFINITY;
 }
 
 __device__ __forceinline__ int offset_at(const BalanceParams& p, int g) {
   return p.offsets ? min(max(p.offsets[g], 0), p.n) : (g ? p.n : 0);
 }
 
-// The first sequence that ends behind token t.
-__device__ __forceinline__ int sequence_of(const BalanceParams& p, int t) {
-  int lo = 0, hi = p.sequences;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offset_at(p, mid + 1) > t)
-      hi = mid;
-    else
-      lo = mid + 1;
+// The first sequence that ends behind token t, and its ends (a whole warp, all lanes the same answer): 128
+// places at a time, as each step is a round trip to L2.
+__device__ __forceinline__ int sequence_of(const BalanceParams& p, int t, int lane, int& from, int& to) {
+  from = 0, to = p.n;
+  if (!p.offsets) return t < p.n ? 0 : p.sequences;
+  int lo = 0, many = p.sequences;            // the answer is in [lo, lo + many]
+  bool known = false;
+  while (many > 0) {
+    const int step = (many + 127) / 128, end = lo + many;
+    int passed = 0, first[4], last[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {            // the last of this lane's stretch, and its ends
+      const int g = lo + (32 * i + lane) * step + step - 1;
+      const bool there = g < end || (g == end && step == 1 && end < p.sequences);
+      first[i] = there && step == 1 ? offset_at(p, g) : 0;
+      last[i] = there ? offset_at(p, g + 1) : 0;
+      passed += __popc(__ballot_sync(kAll, g < end && last[i] <= t));
+    }
+    if (step == 1 && passed < 128) {
+      known = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (passed / 32 == i) from = __shfl_sync(kAll, first[i], passed % 32), to = __shfl_sync(kAll, last[i], passed % 32);
+    }
+    lo = min(lo + passed * step, end);
+    many = step > 1 ? min(step - 1, end - lo) : 0;
   }
+  if (!known && lo < p.sequences) from = offset_at(p, lo), to = offset_at(p, lo + 1);
   return lo;
+}
+
+// A lane's choice of a token, -1 where it is no expert.
+__device__ __forceinline__ int id_of(const BalanceParams& p, int t, int lane) {
+  const int64_t id = p.idx[static_cast<int64_t>(t) * p.topk + lane];
+  return id >= 0 && id < p.experts ? static_cast<int>(id) : -1;
 }
 
 __host__ __device__ __forceinline__ int run_of(int n, int blocks) { return (n + blocks - 1) / blocks; }
 
-template <class T, int V, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kWarps * 32) balance_sums_kernel(BalanceParams p) {
+__device__ __forceinline__ float ld(const float* p) { return ld_coherent(p); }
+
+// A sequence's rows of sums for 32 experts: counts, sums, and the losses' parts.  All WARPS of the
+// block.
+template <int WARPS>
+struct Final {
+  float sums[WARPS][32], squares[WARPS];
+  int counts[WARPS][32], lives[WARPS];
+
+  __device__ __forceinline__ void columns(const BalanceParams& p, int g, int column, int lane, int warp) {
+    const int e = column * kBalanceColumns + lane;
+    const int run = run_of(p.n, p.blocks), from = offset_at(p, g), to = offset_at(p, g + 1), words = 2 * p.experts + 2;
+    // the blocks that have tokens of this sequence
+    const int b0 = to > from ? from / run : 0, b1 = to > from ? (to - 1) / run + 1 : 0;
+    float sum = 0.0f, square = 0.0f;
+    int count = 0, live = 0;
+#pragma unroll 8
+    for (int b = b0 + warp; b < b1; b += WARPS) {
+      const float* row = p.sums + (static_cast<int64_t>(b) + g) * words;
+      if (e < p.experts) sum += ld(row + e), count += __float_as_int(ld(row + p.experts + e));
+      live += __float_as_int(ld(row + 2 * p.experts));
+      square += ld(row + 2 * p.experts + 1);
+    }
+    sums[warp][lane] = sum, counts[warp][lane] = count;
+    if (lane == 0) lives[warp] = live, squares[warp] = square;
+    __syncthreads();
+    if (warp == 0) {
+      sum = square = 0.0f, count = live = 0;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += sums[w][lane], count += counts[w][lane], live += lives[w], square += squares[w];
+      if (e < p.experts) {
+        p.counts[static_cast<int64_t>(g) * p.experts + e] = count;
+        p.prob_sums[static_cast<int64_t>(g) * p.experts + e] = sum;
+      }
+      const float share = live ? static_cast<float>(p.experts) / (static_cast<float>(p.topk) * p.sequences) / live / live : 0.0f;
+      const float dot = warp_sum(e < p.experts ? static_cast<float>(count) * sum : 0.0f) * share;
+      if (lane == 0) {
+        const int columns = (p.experts + kBalanceColumns - 1) / kBalanceColumns;
+        float* part = p.parts + 2 * (static_cast<int64_t>(g) * columns + column);
+        part[0] = dot;
+        part[1] = column ? 0.0f : square;
+        if (column == 0) p.tokens[g] = live;
+      }
+    }
+  }
+
+  // The losses, from the parts of all sequences and columns.
+  __device__ __forceinline__ void losses(const BalanceParams& p, int64_t parts, int lane, int warp) {
+    float loss = 0.0f, z = 0.0f;
+    int total = 0;
+    for (int64_t i = threadIdx.x; i < parts; i += WARPS * 32) loss += ld(p.parts + 2 * i), z += ld(p.parts + 2 * i + 1);
+    for (int i = threadIdx.x; i < p.sequences; i += WARPS * 32) total += ld_coherent(p.tokens + i);
+    loss = warp_sum(loss);
+    z = warp_sum(z);
+    total = __reduce_add_sync(kAll, total);
+    __syncthreads();
+    if (lane == 0) sums[warp][0] = loss, squares[warp] = z, lives[warp] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      loss = z = 0.0f, total = 0;
+      for (int w = 0; w < WARPS; ++w) loss += sums[w][0], z += squares[w], total += lives[w];
+      p.loss[0] = loss;
+      p.loss[1] = total ? z / total : 0.0f;
+      p.tokens[p.sequences] = total;
+    }
+  }
+};
+
+// ALONE: the only block and the only sequence; it writes the outputs itself.
+template <class T, int V, bool VEC, bool SIGMOID, bool ALONE>
+__global__ void __launch_bounds__(sum_warps(V) * 32) balance_sums_kernel(BalanceParams p) {
+  constexpr int kWarps = sum_warps(V), U = at_once(V);
   extern __shared__ float shared[];                  // [kWarps][E] sums, [E] counts
   __shared__ float zz[kWarps];
   __shared__ int live_of[kWarps];
@@ -111,8 +243,8 @@ __global__ void __launch_bounds__(kWarps * 32) balance_sums_kernel(BalanceParams
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int run = run_of(p.n, p.blocks), start = static_cast<int>(blockIdx.x) * run, end = min(start + run, p.n);
   grid_dependency_wait();
-  for (int at = start, g; at < end && (g = sequence_of(p, at)) < p.sequences;) {
-    const int from = max(at, offset_at(p, g)), to = min(end, offset_at(p, g + 1));
+  for (int at = start, g, from, to; at < end && (g = sequence_of(p, at, lane, from, to)) < p.sequences;) {
+    from = max(at, from), to = min(end, to);
     at = max(to, at + 1);
     if (from >= to) continue;
     for (int e = threadIdx.x; e < p.experts; e += kWarps * 32) cnt[e] = 0;
@@ -121,19 +253,37 @@ __global__ void __launch_bounds__(kWarps * 32) balance_sums_kernel(BalanceParams
     int live = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    for (int t = from + warp; t < to; t += kWarps) {
-      float z[V], none[V];
-      load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + t * p.row_stride, p.experts, lane, z);
-      int64_t id = -1;
-      if (lane < p.topk) id = p.idx[static_cast<int64_t>(t) * p.topk + lane];
-      const bool valid = id >= 0 && id < p.experts;
-      if (!__any_sync(kAll, valid)) continue;
-      if (valid) atomicAdd(cnt + id, 1);
-      const float lse = probabilities<V, SIGMOID, false>(z, none, none);
+    float next[U][V];
+    int next_id[U];
+    auto fetch = [&](int t) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += z[v];
-      squares += lse > -INFINITY ? lse * lse : 0.0f;
-      ++live;
+      for (int u = 0; u < U; ++u) {
+        const int mine = min(t + u * kWarps, to - 1);
+        load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + mine * p.row_stride, p.experts, lane, next[u]);
+        next_id[u] = lane < p.topk && t + u * kWarps < to ? id_of(p, mine, lane) : -1;
+      }
+    };
+    if (from + warp < to) fetch(from + warp);
+    for (int t = from + warp; t < to; t += U * kWarps) {
+      float z[U][V], lse[U];
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        id[u] = next_id[u];
+#pragma unroll
+        for (int v = 0; v < V; ++v) z[u][v] = next[u][v];
+      }
+      if (t + U * kWarps < to) fetch(t + U * kWarps);   // under way while these are summed
+      probabilities<U, V, SIGMOID, false>(z, z, z, lse);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!__any_sync(kAll, id[u] >= 0)) continue;
+        if (id[u] >= 0) atomicAdd(cnt + id[u], 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += z[u][v];
+        squares += lse[u] > -INFINITY ? lse[u] * lse[u] : 0.0f;
+        ++live;
+      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -142,174 +292,175 @@ __global__ void __launch_bounds__(kWarps * 32) balance_sums_kernel(BalanceParams
     }
     if (lane == 0) zz[warp] = squares, live_of[warp] = live;
     __syncthreads();
+    float s = 0.0f;
+    int k = 0;
+    if (ALONE || threadIdx.x == 0)
+      for (int w = 0; w < kWarps; ++w) s += zz[w], k += live_of[w];
+    if constexpr (ALONE) {
+      float dot = 0.0f;
+      for (int e = threadIdx.x; e < p.experts; e += kWarps * 32) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += shared[w * p.experts + e];
+        p.prob_sums[e] = sum;
+        p.counts[e] = cnt[e];
+        dot = fmaf(static_cast<float>(cnt[e]), sum, dot);
+      }
+      dot = warp_sum(dot);
+      __syncthreads();                       // zz has been read
+      if (lane == 0) zz[warp] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        dot = 0.0f;
+        for (int w = 0; w < kWarps; ++w) dot += zz[w];
+        p.tokens[0] = p.tokens[1] = k;
+        p.loss[0] = k ? dot * (static_cast<float>(p.experts) / static_cast<float>(p.topk)) / k / k : 0.0f;
+        p.loss[1] = k ? s / k : 0.0f;
+      }
+      return;
+    }
     float* out = p.sums + (static_cast<int64_t>(blockIdx.x) + g) * (2 * p.experts + 2);
     for (int e = threadIdx.x; e < p.experts; e += kWarps * 32) {
-      float s = 0.0f;
+      float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += shared[w * p.experts + e];
-      out[e] = s;
+      for (int w = 0; w < kWarps; ++w) sum += shared[w * p.experts + e];
+      out[e] = sum;
       out[p.experts + e] = __int_as_float(cnt[e]);
     }
-    if (threadIdx.x == 0) {
-      float s = 0.0f;
-      int k = 0;
-      for (int w = 0; w < kWarps; ++w) s += zz[w], k += live_of[w];
-      out[2 * p.experts] = __int_as_float(k);
-      out[2 * p.experts + 1] = s;
-    }
+    if (threadIdx.x == 0) out[2 * p.experts] = __int_as_float(k), out[2 * p.experts + 1] = s;
     __syncthreads();
+  }
+  if constexpr (ALONE) {                     // the sequence has no tokens
+    for (int e = threadIdx.x; e < p.experts; e += kWarps * 32) p.prob_sums[e] = 0.0f, p.counts[e] = 0;
+    if (threadIdx.x < 2) p.tokens[threadIdx.x] = 0, p.loss[threadIdx.x] = 0.0f;
   }
 }
 
-__device__ __forceinline__ float ld(const float* p) { return ld_coherent(p); }
-
-// Sum over the block, in thread 0 (in a fixed order).
-__device__ __forceinline__ float block_sum(float v, float* shared) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-  if (threadIdx.x == 0)
-    for (int w = 0; w < kWarps; ++w) s += shared[w];
-  return s;
-}
-
 // grid: the column blocks of each sequence in turn
-__global__ void __launch_bounds__(kWarps * 32) balance_final_kernel(BalanceParams p) {
-  __shared__ float sums[kWarps][32], red[kWarps];
-  __shared__ int cnts[kWarps][32], lives[kWarps];
+__global__ void __launch_bounds__(kFinalWarps * 32) balance_final_kernel(BalanceParams p) {
+  __shared__ Final<kFinalWarps> f;
   __shared__ bool last;
   allow_dependent_grids();
   const int columns = (p.experts + kBalanceColumns - 1) / kBalanceColumns;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = static_cast<int>(blockIdx.x) / columns, column = static_cast<int>(blockIdx.x) % columns;
-  const int e = column * kBalanceColumns + lane;
   grid_dependency_wait();
-  const int run = run_of(p.n, p.blocks), from = offset_at(p, g), to = offset_at(p, g + 1), words = 2 * p.experts + 2;
-  // the blocks that have tokens of this sequence
-  const int b0 = to > from ? from / run : 0, b1 = to > from ? (to - 1) / run + 1 : 0;
-  float sum = 0.0f, squares = 0.0f;
-  int count = 0, live = 0;
-#pragma unroll 4
-  for (int b = b0 + warp; b < b1; b += kWarps) {
-    const float* row = p.sums + (static_cast<int64_t>(b) + g) * words;
-    if (e < p.experts) sum += ld(row + e), count += __float_as_int(ld(row + p.experts + e));
-    live += __float_as_int(ld(row + 2 * p.experts));
-    squares += ld(row + 2 * p.experts + 1);
-  }
-  sums[warp][lane] = sum, cnts[warp][lane] = count;
-  if (lane == 0) lives[warp] = live, red[warp] = squares;
-  __syncthreads();
-  if (warp == 0) {
-    sum = squares = 0.0f, count = live = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += sums[w][lane], count += cnts[w][lane], live += lives[w], squares += red[w];
-    if (e < p.experts) {
-      p.counts[static_cast<int64_t>(g) * p.experts + e] = count;
-      p.prob_sums[static_cast<int64_t>(g) * p.experts + e] = sum;
-    }
-    const float share = live ? static_cast<float>(p.experts) / (static_cast<float>(p.topk) * p.sequences) / live / live : 0.0f;
-    const float dot = warp_sum(e < p.experts ? static_cast<float>(count) * sum : 0.0f) * share;
-    if (lane == 0) {
-      float* part = p.parts + 2 * static_cast<int64_t>(blockIdx.x);
-      part[0] = dot;
-      part[1] = column ? 0.0f : squares;
-      if (column == 0) p.tokens[g] = live;
-      __threadfence();
-      last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
-    }
+  f.columns(p, static_cast<int>(blockIdx.x) / columns, static_cast<int>(blockIdx.x) % columns, lane, warp);
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  float loss = 0.0f, z = 0.0f;
-  int total = 0;
-  for (int64_t i = threadIdx.x; i < gridDim.x; i += kWarps * 32) loss += ld(p.parts + 2 * i), z += ld(p.parts + 2 * i + 1);
-  for (int i = threadIdx.x; i < p.sequences; i += kWarps * 32) total += ld_coherent(p.tokens + i);
-  loss = block_sum(loss, red);
-  z = block_sum(z, red);
-  total = __reduce_add_sync(kAll, total);
-  __syncthreads();
-  if (lane == 0) lives[warp] = total;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    total = 0;
-    for (int w = 0; w < kWarps; ++w) total += lives[w];
-    p.loss[0] = loss;
-    p.loss[1] = total ? z / total : 0.0f;
-    p.tokens[p.sequences] = total;
-    *p.ticket = 0;
-  }
+  f.losses(p, gridDim.x, lane, warp);
+  if (threadIdx.x == 0) *p.ticket = 0;
 }
 
 template <class T, int V, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kWarps * 32) balance_backward_kernel(BalanceParams p) {
+__global__ void __launch_bounds__(kBackWarps * 32) balance_backward_kernel(BalanceParams p, int tokens) {
+  constexpr int U = at_once(V);
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int start = (blockIdx.x * kBackWarps + static_cast<int>(threadIdx.x >> 5)) * tokens;
   grid_dependency_wait();
-  if (t >= p.n) return;
-  const int g = sequence_of(p, t);
-  if (g >= p.sequences || t < offset_at(p, g)) return;
-  float z[V], soft[V], not_s[V], d[V];
-  load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + t * p.row_stride, p.experts, lane, z);
-  int64_t id = -1;
-  if (lane < p.topk) id = p.idx[static_cast<int64_t>(t) * p.topk + lane];
-  const bool live = __any_sync(kAll, id >= 0 && id < p.experts);
-  T* out = static_cast<T*>(p.grad) + t * p.grad_stride;
-  if (live) {
-    const int tg = p.tokens_in[g], total = p.tokens_in[p.sequences];
+  const int end = min(start + tokens, p.n);
+  if (start >= end) return;
+  const int total = p.tokens_in[p.sequences];
+  const float gb = p.grad_loss[0], gz = total > 0 ? p.grad_loss[1] * 2.0f / total : 0.0f;
+  for (int at = start, g, from, to; at < end && (g = sequence_of(p, at, lane, from, to)) < p.sequences;) {
+    from = max(at, from), to = min(end, to);
+    at = max(to, at + 1);
+    if (from >= to) continue;
+    const int tg = p.tokens_in[g];
     // sum p = 1, so any constant may be taken from the counts; their mean leaves the most bits
     const int mean = static_cast<int>(static_cast<int64_t>(tg) * p.topk / p.experts);
+    const float share = tg > 0 ? gb * (static_cast<float>(p.experts) / (static_cast<float>(p.topk) * p.sequences)) / tg / tg : 0.0f;
     float c[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int j = expert_of<VEC, V>(lane, v);
       c[v] = j < p.experts ? static_cast<float>(p.counts_in[static_cast<int64_t>(g) * p.experts + j] - mean) : 0.0f;
     }
-    const float lse = probabilities<V, SIGMOID, true>(z, soft, not_s);
-    float dot = 0.0f;
+    float next[U][V];
+    int next_id[U];
+    auto fetch = [&](int t) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) dot = fmaf(c[v], z[v], dot);
-    dot = warp_sum(dot);
-    const float share = tg > 0 ? p.grad_loss[0] * (static_cast<float>(p.experts) / (static_cast<float>(p.topk) * p.sequences)) / tg / tg : 0.0f;
-    const float rise = total > 0 && lse > -INFINITY ? p.grad_loss[1] * 2.0f * lse / total : 0.0f;
+      for (int u = 0; u < U; ++u) {
+        const int mine = min(t + u, to - 1);
+        load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + mine * p.row_stride, p.experts, lane, next[u]);
+        next_id[u] = lane < p.topk ? id_of(p, mine, lane) : -1;
+      }
+    };
+    fetch(from);
+#pragma unroll 1
+    for (int t = from; t < to; t += U) {
+      float z[U][V], soft[SIGMOID ? U : 1][SIGMOID ? V : 1], not_s[SIGMOID ? U : 1][SIGMOID ? V : 1], lse[U], dot[U];
+      int id[U];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float s = SIGMOID ? soft[v] : z[v];
-      d[v] = share * z[v] * (c[v] - dot);
-      if constexpr (SIGMOID) d[v] *= not_s[v];
-      d[v] = s > 0.0f ? fmaf(rise, s, d[v]) : (z[v] > 0.0f ? d[v] : 0.0f);
-    }
-  } else {
-    if (p.accumulate) return;
+      for (int u = 0; u < U; ++u) {
+        id[u] = next_id[u];
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = 0.0f;
-  }
-  if (p.accumulate) {
+        for (int v = 0; v < V; ++v) z[u][v] = next[u][v];
+      }
+      if (t + U < to) fetch(t + U);          // under way while these are worked on
+      if constexpr (SIGMOID)
+        probabilities<U, V, true, true>(z, soft, not_s, lse);
+      else
+        probabilities<U, V, false, true>(z, z, z, lse);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = expert_of<VEC, V>(lane, v);
-      if (j < p.experts) d[v] += as_float(out[j]);
-    }
-  }
-  if constexpr (VEC) {
-    store_row<T, V>(out, p.experts, lane, true, d);
-  } else {
+      for (int u = 0; u < U; ++u) {
+        dot[u] = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int j = 32 * v + lane;
-      if (j < p.experts) out[j] = from_float<T>(d[v]);
+        for (int v = 0; v < V; ++v) dot[u] = fmaf(c[v], z[u][v], dot[u]);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(kAll, dot[u], d);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= to) break;
+        const bool live = __any_sync(kAll, id[u] >= 0);
+        if (!live && p.accumulate) continue;
+        T* out = static_cast<T*>(p.grad) + (t + u) * p.grad_stride;
+        const float rise = lse[u] > -INFINITY ? gz * lse[u] : 0.0f;
+        float d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float q = z[u][v];
+          float s = q;
+          if constexpr (SIGMOID) s = soft[u][v];
+          d[v] = share * q * (c[v] - dot[u]);
+          if constexpr (SIGMOID) d[v] *= not_s[u][v];
+          d[v] = s > 0.0f ? fmaf(rise, s, d[v]) : (q > 0.0f ? d[v] : 0.0f);
+          if (!live) d[v] = 0.0f;
+        }
+        if (p.accumulate) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int j = expert_of<VEC, V>(lane, v);
+            if (j < p.experts) d[v] += as_float(out[j]);
+          }
+        }
+        if constexpr (VEC) {
+          store_row<T, V>(out, p.experts, lane, true, d);
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int j = 32 * v + lane;
+            if (j < p.experts) out[j] = from_float<T>(d[v]);
+          }
+        }
+      }
     }
   }
 }
 
-template <class K>
-cudaError_t launch_pdl(K kernel, dim3 grid, size_t smem, cudaStream_t s, const BalanceParams& p) {
+template <class... A, class... B>
+cudaError_t launch_pdl(void (*kernel)(A...), unsigned grid, int warps, size_t smem, cudaStream_t s, const B&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -318,19 +469,28 @@ cudaError_t launch_pdl(K kernel, dim3 grid, size_t smem, cudaStream_t s, const B
   static const bool pdl = PdlEnabled();
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A>(args)...);
+}
+
+template <class T, int V, bool VEC, bool SIGMOID, bool ALONE>
+cudaError_t launch_sums(const BalanceParams& p, cudaStream_t s) {
+  const size_t smem = (sum_warps(V) + 1) * static_cast<size_t>(p.experts) * 4;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(balance_sums_kernel<T, V, VEC, SIGMOID, ALONE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(balance_sums_kernel<T, V, VEC, SIGMOID, ALONE>, p.blocks, sum_warps(V), smem, s, p);
 }
 
 template <class T, int V, bool VEC, bool SIGMOID>
 cudaError_t launch_one(const BalanceParams& p, bool backward, cudaStream_t s) {
-  if (backward) return launch_pdl(balance_backward_kernel<T, V, VEC, SIGMOID>, dim3((p.n + kWarps - 1) / kWarps), 0, s, p);
-  const size_t smem = (kWarps + 1) * static_cast<size_t>(p.experts) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(balance_sums_kernel<T, V, VEC, SIGMOID>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  if (backward) {
+    // 32 warps an SM, and no more than 8 tokens each
+    const int tokens = std::min(std::max(p.n / (32 * p.num_sms), at_once(V)), 8), per = kBackWarps * tokens;
+    return launch_pdl(balance_backward_kernel<T, V, VEC, SIGMOID>, (p.n + per - 1) / per, kBackWarps, 0, s, p, tokens);
   }
-  return launch_pdl(balance_sums_kernel<T, V, VEC, SIGMOID>, dim3(p.blocks), smem, s, p);
+  return BalanceAlone(p) ? launch_sums<T, V, VEC, SIGMOID, true>(p, s) : launch_sums<T, V, VEC, SIGMOID, false>(p, s);
 }
 
 template <class T, int V>
@@ -355,16 +515,20 @@ cudaError_t launch(const BalanceParams& p, bool backward, cudaStream_t s) {
 
 }  // namespace
 
-int BalanceBlocks(int n, int num_sms) {
-  const int most = 4 * num_sms, some = (n + kWarps - 1) / kWarps;
+// One block of the first kernel an SM up to 256 experts, and as many warps beyond; two rounds of
+// its warps at least, unless that leaves a single block.
+int BalanceBlocks(int n, int experts, int num_sms) {
+  const int warps = experts <= 256 ? 32 : experts <= 512 ? 16 : 8;
+  const int most = num_sms * (32 / warps), some = (n + 2 * warps - 1) / (2 * warps);
   return some < 1 ? 1 : some < most ? some : most;
 }
 
 cudaError_t LaunchBalance(const BalanceParams& p, cudaStream_t s) {
   if (p.n > 0)
-    if (const cudaError_t e = p.bf16 ? launch<__nv_bfloat16>(p, false, s) : launch<float>(p, false, s); e != cudaSuccess)
+    if (const cudaError_t e = p.bf16 ? launch<__nv_bfloat16>(p, false, s) : launch<float>(p, false, s);
+        e != cudaSuccess || BalanceAlone(p))
       return e;
-  return launch_pdl(balance_final_kernel, dim3(static_cast<unsigned>(BalancePartWords(p.sequences, p.experts) / 2)), 0, s, p);
+  return launch_pdl(balance_final_kernel, static_cast<unsigned>(BalancePartWords(p.sequences, p.experts) / 2), kFinalWarps, 0, s, p);
 }
 
 cudaError_t LaunchBalanceBackward(const BalanceParams& p, cudaStream_t s) {

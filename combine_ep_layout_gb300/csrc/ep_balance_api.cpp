@@ -71,7 +71,8 @@ int check_common(ep_balance_t b, const void* logits, int32_t dtype, int64_t row_
   p->sums = b->sums;
   p->parts = b->parts;
   p->ticket = b->ticket;
-  p->blocks = BalanceBlocks(n, b->num_sms);
+  p->num_sms = b->num_sms;
+  p->blocks = BalanceBlocks(n, p->experts, b->num_sms);
   return EP_OK;
 }
 
@@ -104,7 +105,7 @@ int ep_balance_create(const ep_route_cfg_t* route, int32_t max_tokens, int32_t m
     if ((e = cudaGetDevice(&b->device)) != cudaSuccess) return bail(fail_cuda(e, "cudaGetDevice"));
     if ((e = cudaDeviceGetAttribute(&b->num_sms, cudaDevAttrMultiProcessorCount, b->device)) != cudaSuccess)
       return bail(fail_cuda(e, "cudaDeviceGetAttribute"));
-    const size_t sums = BalanceSumWords(BalanceBlocks(max_tokens, b->num_sms), max_sequences, route->num_experts);
+    const size_t sums = BalanceSumWords(BalanceBlocks(max_tokens, route->num_experts, b->num_sms), max_sequences, route->num_experts);
     const size_t parts = BalancePartWords(max_sequences, route->num_experts);
     const size_t total = (sums + parts + 1) * sizeof(float);
     if ((e = cudaStreamCreateWithFlags(&b->own_stream, cudaStreamNonBlocking)) != cudaSuccess)

@@ -35,19 +35,23 @@ struct BalanceParams {
   float* parts;             // [G, column blocks, 2]
   int32_t* ticket;          // [1], zero between launches
   int blocks;               // of the first kernel
+  int num_sms;
 };
 
 // Experts that one final block adds up.
 constexpr int kBalanceColumns = 32;
 
 // Blocks of the first kernel for n tokens, and the workspace's sizes in words.
-int BalanceBlocks(int n, int num_sms);
+int BalanceBlocks(int n, int experts, int num_sms);
 inline size_t BalanceSumWords(int blocks, int sequences, int experts) {
   return (static_cast<size_t>(blocks) + sequences) * (2 * static_cast<size_t>(experts) + 2);
 }
 inline size_t BalancePartWords(int sequences, int experts) {
   return static_cast<size_t>(sequences) * ((experts + kBalanceColumns - 1) / kBalanceColumns) * 2;
 }
+
+// Whether the first kernel's one block does everything.
+inline bool BalanceAlone(const BalanceParams& p) { return p.n > 0 && p.blocks == 1 && p.sequences == 1; }
 
 cudaError_t LaunchBalance(const BalanceParams& p, cudaStream_t s);
 cudaError_t LaunchBalanceBackward(const BalanceParams& p, cudaStream_t s);

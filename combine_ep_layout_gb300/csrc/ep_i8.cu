@@ -2,8 +2,8 @@
 // receive rows of a layout (include/ep_gb300_i8.h states the formulas).
 //
 // Bound by reading the rows once and writing what comes of them.  A group of
-// threads holds a row in registers between the search of its largest magnitude and the
-// rounding, so that x is read once; rows of more than 16384 columns are read a second time, out
+// threads holds a row in registers, 16 values each (32 where rows have more than 8192), between the search
+// of its largest magnitude and the rounding, so that x is read once; rows of more than 16384 columns are read a second time, out
 // of L2.  The magnitude is searched as an unsigned integer, where infinities and NaNs
 // are above every number.
 #include <cuda_bf16.h>
@@ -22,7 +22,6 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kVec = 16;      // columns of one vector: 16 bytes of int8
-constexpr int kMine = 2;      // vectors that a thread holds
 
 // 16 values of a row as floats.
 template <class T, bool ALIGNED>
@@ -77,9 +76,10 @@ __device__ __forceinline__ uint4 round16(const float (&v)[kVec], float s, float 
 }
 
 // G threads a row, 128 / G rows a block where G is below 128.
-template <class T, int G, bool ALIGNED>
-__global__ void __launch_bounds__(G < 128 ? 128 : G) i8_rows_kernel(I8RowsParams p) {
+template <class T, int G, int MINE, bool ALIGNED>
+__global__ void __launch_bounds__(G < 128 ? 128 : G, (MINE == 1 ? 1536 : 1024) / (G < 128 ? 128 : G)) i8_rows_kernel(I8RowsParams p) {
   constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G;
+  constexpr bool kMore = MINE == 2;           // rows may have more vectors than the threads hold
   __shared__ unsigned most[2][kThreads / 32];
   allow_dependent_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = threadIdx.x / G, at = threadIdx.x % G;
@@ -92,16 +92,19 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) i8_rows_kernel(I8RowsParams
     const int64_t row = r0 + group;
     const bool ok = row < rows && (!p.meta || ld_coherent(p.meta + row * p.meta_stride) >= 0);
     const T* x = static_cast<const T*>(p.x) + row * p.row_stride;
-    float v[kMine][kVec];
+    // lane k: the k-th row that this one goes to
+    int slot = -1;
+    if (p.slots && ok && lane < p.topk) slot = ld_coherent(p.slots + row * p.topk + lane);
+    float v[MINE][kVec];
     unsigned m = 0;
 #pragma unroll
-    for (int u = 0; u < kMine; ++u)
+    for (int u = 0; u < MINE; ++u)
       if (ok && at + u * G < vectors) {
         load16<T, ALIGNED>(x + static_cast<int64_t>(at + u * G) * kVec, v[u]);
         m = max(m, magnitude(v[u]));
       }
-    if (G == 512)
-      for (int c = at + kMine * G; ok && c < vectors; c += G) {
+    if constexpr (kMore)
+      for (int c = at + MINE * G; ok && c < vectors; c += G) {
         float more[kVec];
         load16<T, ALIGNED>(x + static_cast<int64_t>(c) * kVec, more);
         m = max(m, magnitude(more));
@@ -110,45 +113,43 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) i8_rows_kernel(I8RowsParams
     if constexpr (G > 32) {
       if (lane == 0) most[turn][warp] = m;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < G / 32; ++w) m = max(m, most[turn][group * (G / 32) + w]);
+      m = __reduce_max_sync(kAll, lane < G / 32 ? most[turn][group * (G / 32) + lane] : 0u);
     }
-    if (!ok) continue;
+    if (!ok) continue;                         // the same for a whole warp
     const bool fine = m < 0x7f800000u;
     const float s = fine ? __fdiv_rn(__uint_as_float(m), 127.0f) : __uint_as_float(0x7fc00000u);
     const float inv = fine ? 1.0f / s : 0.0f;
     auto store = [&](int c, const float(&a)[kVec]) {
-      const uint4 q = fine ? round16(a, s, inv) : make_uint4(0, 0, 0, 0);
+      const bool mine = c < vectors;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (mine && fine) q = round16(a, s, inv);
+      int8_t* to = p.q + static_cast<int64_t>(c) * kVec;
       if (!p.slots) {
-        *reinterpret_cast<uint4*>(p.q + row * p.cols + static_cast<int64_t>(c) * kVec) = q;
+        if (mine) *reinterpret_cast<uint4*>(to + row * p.cols) = q;
       } else {
         for (int k = 0; k < p.topk; ++k) {
-          const int d = ld_coherent(p.slots + row * p.topk + k);
-          if (d >= 0) *reinterpret_cast<uint4*>(p.q + static_cast<int64_t>(d) * p.cols + static_cast<int64_t>(c) * kVec) = q;
+          const int d = __shfl_sync(kAll, slot, k);
+          if (d >= 0 && mine) *reinterpret_cast<uint4*>(to + static_cast<int64_t>(d) * p.cols) = q;
         }
       }
     };
 #pragma unroll
-    for (int u = 0; u < kMine; ++u)
-      if (at + u * G < vectors) store(at + u * G, v[u]);
-    if (G == 512)
-      for (int c = at + kMine * G; c < vectors; c += G) {
+    for (int u = 0; u < MINE; ++u) store(at + u * G, v[u]);
+    if constexpr (kMore)
+      for (int c0 = MINE * G; c0 < vectors; c0 += G) {
         float more[kVec];
-        load16<T, ALIGNED>(x + static_cast<int64_t>(c) * kVec, more);
-        store(c, more);
+        if (c0 + at < vectors) load16<T, ALIGNED>(x + static_cast<int64_t>(c0 + at) * kVec, more);
+        store(c0 + at, more);
       }
     if (!p.slots) {
       if (at == 0) p.scales[row] = s;
-    } else {
-      for (int k = at; k < p.topk; k += G) {
-        const int d = ld_coherent(p.slots + row * p.topk + k);
-        if (d >= 0) p.scales[d] = s;
-      }
+    } else if (at < 32 && slot >= 0) {
+      p.scales[slot] = s;
     }
   }
 }
 
-template <class T, int G>
+template <class T, int G, int MINE = 1>
 cudaError_t launch_g(const I8RowsParams& p, cudaStream_t s) {
   constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G;
   const bool vec = rows::aligned16(p.x, p.row_stride * static_cast<int64_t>(sizeof(T)));
@@ -163,17 +164,18 @@ cudaError_t launch_g(const I8RowsParams& p, cudaStream_t s) {
   static const bool pdl = PdlEnabled();
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return vec ? cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, true>, p) : cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, false>, p);
+  return vec ? cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, true>, p) : cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, false>, p);
 }
 
 template <class T>
 cudaError_t launch(const I8RowsParams& p, cudaStream_t s) {
   const int vectors = p.cols / kVec;
-  if (vectors <= 32 * kMine) return launch_g<T, 32>(p, s);
-  if (vectors <= 64 * kMine) return launch_g<T, 64>(p, s);
-  if (vectors <= 128 * kMine) return launch_g<T, 128>(p, s);
-  if (vectors <= 256 * kMine) return launch_g<T, 256>(p, s);
-  return launch_g<T, 512>(p, s);
+  if (vectors <= 32) return launch_g<T, 32>(p, s);
+  if (vectors <= 64) return launch_g<T, 64>(p, s);
+  if (vectors <= 128) return launch_g<T, 128>(p, s);
+  if (vectors <= 256) return launch_g<T, 256>(p, s);
+  if (vectors <= 512) return launch_g<T, 512>(p, s);
+  return launch_g<T, 512, 2>(p, s);
 }
 
 }  // namespace
