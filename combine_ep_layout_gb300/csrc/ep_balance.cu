@@ -5,14 +5,14 @@
 // exp (sigmoid: two).
 //
 // Forward, two launches: each block of the first takes a run of consecutive
-// tokens, a warp two tokens at a time (the next two under way), and keeps a column of sums in every lane; for each
+// tokens, a warp a few tokens at a time, and keeps a column of sums in every lane; for each
 // sequence that its run touches it writes one row of sums (probabilities, counts,
 // live tokens, squared lse).  The second adds those rows, 32 experts a block, and the last of its
 // blocks adds the losses.  Few tokens of one sequence: one block does both.  The
 // pairs (block, sequence) with tokens form a staircase, so block + sequence numbers their
 // rows.  Every sum has a fixed order; only whole numbers go through atomics.
 //
-// Backward: a warp takes up to 8 consecutive tokens, two at a time and the next two under way, with the counts of their
+// Backward: a warp takes up to 8 consecutive tokens, a few at a time, with the counts of their
 // sequence in registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,10 +34,10 @@ using namespace route;
 using namespace rows;
 
 constexpr int kFinalWarps = 16, kBackWarps = 8;
-// Warps of a block of sums: registers allow 32 of them up to 256 experts.  Two rows at a time up to
-// there, one beyond.
+// Warps of a block of sums: registers allow 32 of them up to 256 experts.  Four rows at a time up to 128
+// experts, two up to 256, one beyond.
 __host__ __device__ constexpr int sum_warps(int v) { return v <= 8 ? 32 : v == 16 ? 16 : 8; }
-__host__ __device__ constexpr int at_once(int v) { return v <= 8 ? 2 : 1; }
+__host__ __device__ constexpr int at_once(int v) { return v <= 4 ? 4 : v == 8 ? 2 : 1; }
 
 // A lane's scores of a row.  VEC: V consecutive ones; else every 32nd, which rows that are not
 // 16-byte aligned are read by in whole sectors.
@@ -59,14 +59,11 @@ __device__ __forceinline__ void load_scores(const T* row, int experts, int lane,
   }
 }
 
-// exp(x), x <= 0 or a finite sigmoid's argument: off by 2^-22 and the rounding of x log2(e).
-__device__ __forceinline__ float exp_fast(float x) {
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_of(float x) {
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
   return e;
-}
-__device__ __forceinline__ float below(float z, float peak) {
-  return z > -INFINITY ? (z == peak ? 1.0f : exp_fast(z - peak)) : 0.0f;
 }
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
@@ -74,31 +71,48 @@ __device__ __forceinline__ float reciprocal(float x) {
   return r;
 }
 
-// U rows: z becomes p; lse is -inf where every score is masked.  SIGMOID and GRAD: soft gets
-// exp(z - lse), not_s 1 - sigmoid(z).
-template <int U, int V, bool SIGMOID, bool GRAD>
-__device__ __forceinline__ void probabilities(float (&z)[U][V], float (&soft)[U][V], float (&not_s)[U][V], float (&lse)[U]) {
-  float peak[U], whole[U], part[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) peak[u] = warp_max(lane_max(z[u]));
+// U rows: z becomes p; peak and whole (the sum of exp(z - peak), 0 where every score is masked) give
+// lse.  SIGMOID and GRAD: soft gets exp(z - lse), not_s 1 - sigmoid(z).  An exponential is one fma and one
+// ex2 (off by 2^-22 and by the rounding of peak log2(e), which all of a row share); rows whose peak is
+// infinite or next to it are subtracted first.
+template <int U, int V, bool SIGMOID, bool GRAD, int SU, int SV>
+__device__ __forceinline__ void probabilities(float (&z)[U][V], float (&soft)[SU][SV], float (&not_s)[SU][SV], float (&peak)[U],
+                                              float (&whole)[U]) {
+  float part[U];
+  bool plain = true;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    peak[u] = warp_max(lane_max(z[u]));
+    plain = plain && fabsf(peak[u]) < 1e30f;
     whole[u] = part[u] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float x = z[u][v], e = below(x, peak[u]);
-      whole[u] += e;
-      if constexpr (SIGMOID) {
-        // scaled by exp(-peak) where every score is below zero, so that ratios survive
-        const float t = exp_fast(-fabsf(x)), inv = reciprocal(1.0f + t);
-        const float s = peak[u] < 0.0f ? e * inv : x >= 0.0f ? inv : t * inv;
-        if constexpr (GRAD) soft[u][v] = e, not_s[u][v] = x >= 0.0f ? t * inv : inv;
-        z[u][v] = x > -INFINITY ? s : 0.0f;
-        part[u] += z[u][v];
-      } else {
-        z[u][v] = e;
-      }
+  }
+  const auto score = [&](int u, int v, float e) {
+    whole[u] += e;
+    if constexpr (SIGMOID) {
+      // scaled by exp(-peak) where every score is below zero, so that ratios survive
+      const float x = z[u][v], t = exp2_of(-fabsf(x) * kLog2e), inv = reciprocal(1.0f + t);
+      if constexpr (GRAD) soft[u][v] = e, not_s[u][v] = x >= 0.0f ? t * inv : inv;
+      z[u][v] = peak[u] < 0.0f ? e * inv : x >= 0.0f ? inv : t * inv;
+      part[u] += z[u][v];
+    } else {
+      z[u][v] = e;
     }
+  };
+  if (plain) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float c = -peak[u] * kLog2e;
+#pragma unroll
+      for (int v = 0; v < V; ++v) score(u, v, exp2_of(fmaf(z[u][v], kLog2e, c)));
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = z[u][v];
+        score(u, v, x > -INFINITY ? (x == peak[u] ? 1.0f : exp2_of((x - peak[u]) * kLog2e)) : 0.0f);
+      }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1)
@@ -109,16 +123,17 @@ __device__ __forceinline__ void probabilities(float (&z)[U][V], float (&soft)[U]
     }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float inv = whole[u] > 0.0f ? 1.0f / whole[u] : 0.0f;
-    const float inv_p = SIGMOID ? (part[u] > 0.0f ? 1.0f / part[u] : 0.0f) : inv;
+    const float inv = whole[u] > 0.0f ? reciprocal(whole[u]) : 0.0f;
+    const float inv_p = SIGMOID ? (part[u] > 0.0f ? reciprocal(part[u]) : 0.0f) : inv;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       z[u][v] *= inv_p;
       if constexpr (SIGMOID && GRAD) soft[u][v] *= inv;
     }
-    lse[u] = whole[u] > 0.0f ? peak[u] + logf(whole[u]) : -INFINITY;
   }
 }
+
+__device__ __forceinline__ float lse_of(float peak, float whole) { return whole > 0.0f ? peak + logf(whole) : -INFINITY; }
 
 __device__ __forceinline__ int offset_at(const BalanceParams& p, int g) {
   return p.offsets ? min(max(p.offsets[g], 0), p.n) : (g ? p.n : 0);
@@ -155,10 +170,19 @@ __device__ __forceinline__ int sequence_of(const BalanceParams& p, int t, int la
   return lo;
 }
 
+// Brings a run of rows to L2 ahead of everything that the first loads wait for (a hint).
+template <class T>
+__device__ __forceinline__ void prefetch_rows(const BalanceParams& p, int start, int end) {
+  if (start >= end || p.row_stride > 2 * p.experts) return;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + start * p.row_stride) & ~static_cast<uintptr_t>(15);
+  const uintptr_t b = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + (end - 1) * p.row_stride + p.experts);
+  prefetch_l2(reinterpret_cast<const void*>(a), static_cast<uint32_t>((b - a) & ~static_cast<uintptr_t>(15)));
+}
+
 // A lane's choice of a token, -1 where it is no expert.
-__device__ __forceinline__ int id_of(const BalanceParams& p, int t, int lane) {
-  const int64_t id = p.idx[static_cast<int64_t>(t) * p.topk + lane];
-  return id >= 0 && id < p.experts ? static_cast<int>(id) : -1;
+__device__ __forceinline__ int id_of(const BalanceParams& p, const int64_t* at) {
+  const uint64_t id = static_cast<uint64_t>(*at);
+  return id < static_cast<uint64_t>(p.experts) ? static_cast<int>(id) : -1;
 }
 
 __host__ __device__ __forceinline__ int run_of(int n, int blocks) { return (n + blocks - 1) / blocks; }
@@ -242,10 +266,20 @@ __global__ void __launch_bounds__(sum_warps(V) * 32) balance_sums_kernel(Balance
   int* cnt = reinterpret_cast<int*>(shared + kWarps * p.experts);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int run = run_of(p.n, p.blocks), start = static_cast<int>(blockIdx.x) * run, end = min(start + run, p.n);
+  if (threadIdx.x == 0) prefetch_rows<T>(p, start, end);
   grid_dependency_wait();
-  for (int at = start, g, from, to; at < end && (g = sequence_of(p, at, lane, from, to)) < p.sequences;) {
-    from = max(at, from), to = min(end, to);
+  __shared__ int found[3];
+  for (int at = start; at < end;) {
+    if (warp == 0) {                         // one warp searches for all
+      int from, to;
+      const int g = sequence_of(p, at, lane, from, to);
+      if (lane == 0) found[0] = g, found[1] = max(at, from), found[2] = min(end, to);
+    }
+    __syncthreads();
+    const int g = found[0], from = found[1], to = found[2];
+    if (g >= p.sequences) break;
     at = max(to, at + 1);
+    __syncthreads();
     if (from >= to) continue;
     for (int e = threadIdx.x; e < p.experts; e += kWarps * 32) cnt[e] = 0;
     __syncthreads();
@@ -253,38 +287,40 @@ __global__ void __launch_bounds__(sum_warps(V) * 32) balance_sums_kernel(Balance
     int live = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    float next[U][V];
-    int next_id[U];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int mine = min(t + u * kWarps, to - 1);
-        load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + mine * p.row_stride, p.experts, lane, next[u]);
-        next_id[u] = lane < p.topk && t + u * kWarps < to ? id_of(p, mine, lane) : -1;
-      }
+    // lane i has peak and whole of the warp's i-th live token, until 32 of them are there
+    float my_peak = 0.0f, my_whole = 0.0f;
+    const auto square = [&] {
+      const float lse = lse_of(my_peak, my_whole);
+      if (lse > -INFINITY) squares = fmaf(lse, lse, squares);
+      my_whole = 0.0f;
     };
-    if (from + warp < to) fetch(from + warp);
+    const T* row = static_cast<const T*>(p.logits) + (from + warp) * p.row_stride;
+    const int64_t* ids = p.idx + static_cast<int64_t>(from + warp) * p.topk + lane;
+    const int64_t rows_on = kWarps * p.row_stride, ids_on = static_cast<int64_t>(kWarps) * p.topk;
+    const bool chooses = lane < p.topk;
     for (int t = from + warp; t < to; t += U * kWarps) {
-      float z[U][V], lse[U];
+      float z[U][V], peak[U], whole[U];
       int id[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        id[u] = next_id[u];
-#pragma unroll
-        for (int v = 0; v < V; ++v) z[u][v] = next[u][v];
+        const bool there = u == 0 || t + u * kWarps < to;
+        load_scores<T, V, VEC>(there ? row : static_cast<const T*>(p.logits), p.experts, lane, z[u]);
+        id[u] = chooses && there ? id_of(p, ids) : -1;
+        row += rows_on, ids += ids_on;
       }
-      if (t + U * kWarps < to) fetch(t + U * kWarps);   // under way while these are summed
-      probabilities<U, V, SIGMOID, false>(z, z, z, lse);
+      probabilities<U, V, SIGMOID, false>(z, z, z, peak, whole);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!__any_sync(kAll, id[u] >= 0)) continue;
         if (id[u] >= 0) atomicAdd(cnt + id[u], 1);
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] += z[u][v];
-        squares += lse[u] > -INFINITY ? lse[u] * lse[u] : 0.0f;
-        ++live;
+        if (lane == (live & 31)) my_peak = peak[u], my_whole = whole[u];
+        if ((++live & 31) == 0) square();
       }
     }
+    square();
+    squares = warp_sum(squares);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int j = expert_of<VEC, V>(lane, v);
@@ -357,8 +393,8 @@ __global__ void __launch_bounds__(kFinalWarps * 32) balance_final_kernel(Balance
 }
 
 template <class T, int V, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kBackWarps * 32) balance_backward_kernel(BalanceParams p, int tokens) {
-  constexpr int U = at_once(V);
+__global__ void __launch_bounds__(kBackWarps * 32, V <= 8 ? 6 : 1) balance_backward_kernel(BalanceParams p, int tokens) {
+  constexpr int U = V <= 4 ? 2 : 1;          // more registers cost more than they bring (256 experts, two rows: 24 us, one: 20)
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
   const int start = (blockIdx.x * kBackWarps + static_cast<int>(threadIdx.x >> 5)) * tokens;
@@ -381,32 +417,23 @@ __global__ void __launch_bounds__(kBackWarps * 32) balance_backward_kernel(Balan
       const int j = expert_of<VEC, V>(lane, v);
       c[v] = j < p.experts ? static_cast<float>(p.counts_in[static_cast<int64_t>(g) * p.experts + j] - mean) : 0.0f;
     }
-    float next[U][V];
-    int next_id[U];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int mine = min(t + u, to - 1);
-        load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + mine * p.row_stride, p.experts, lane, next[u]);
-        next_id[u] = lane < p.topk ? id_of(p, mine, lane) : -1;
-      }
-    };
-    fetch(from);
 #pragma unroll 1
     for (int t = from; t < to; t += U) {
-      float z[U][V], soft[SIGMOID ? U : 1][SIGMOID ? V : 1], not_s[SIGMOID ? U : 1][SIGMOID ? V : 1], lse[U], dot[U];
+      float z[U][V], soft[SIGMOID ? U : 1][SIGMOID ? V : 1], not_s[SIGMOID ? U : 1][SIGMOID ? V : 1], peak[U], whole[U], dot[U];
       int id[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        id[u] = next_id[u];
-#pragma unroll
-        for (int v = 0; v < V; ++v) z[u][v] = next[u][v];
+        const int mine = min(t + u, to - 1);
+        load_scores<T, V, VEC>(static_cast<const T*>(p.logits) + mine * p.row_stride, p.experts, lane, z[u]);
+        id[u] = lane < p.topk ? id_of(p, p.idx + static_cast<int64_t>(mine) * p.topk + lane) : -1;
       }
-      if (t + U < to) fetch(t + U);          // under way while these are worked on
-      if constexpr (SIGMOID)
-        probabilities<U, V, true, true>(z, soft, not_s, lse);
-      else
-        probabilities<U, V, false, true>(z, z, z, lse);
+      probabilities<U, V, SIGMOID, true>(z, soft, not_s, peak, whole);
+      // one logarithm for all of them: lane u's is the u-th's
+      float my_lse = 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (lane == u || U == 1) my_lse = whole[u];
+      const float my_log = logf(my_lse);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         dot[u] = 0.0f;
@@ -423,16 +450,15 @@ __global__ void __launch_bounds__(kBackWarps * 32) balance_backward_kernel(Balan
         const bool live = __any_sync(kAll, id[u] >= 0);
         if (!live && p.accumulate) continue;
         T* out = static_cast<T*>(p.grad) + (t + u) * p.grad_stride;
-        const float rise = lse[u] > -INFINITY ? gz * lse[u] : 0.0f;
+        const float lse = peak[u] + __shfl_sync(kAll, my_log, U == 1 ? 0 : u), rise = whole[u] > 0.0f ? gz * lse : 0.0f;
         float d[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float q = z[u][v];
-          float s = q;
-          if constexpr (SIGMOID) s = soft[u][v];
-          d[v] = share * q * (c[v] - dot[u]);
-          if constexpr (SIGMOID) d[v] *= not_s[u][v];
-          d[v] = s > 0.0f ? fmaf(rise, s, d[v]) : (q > 0.0f ? d[v] : 0.0f);
+          if constexpr (SIGMOID)
+            d[v] = share * q * (c[v] - dot[u]) * not_s[u][v] + (soft[u][v] > 0.0f ? rise * soft[u][v] : 0.0f);
+          else
+            d[v] = q > 0.0f ? q * fmaf(share, c[v] - dot[u], rise) : 0.0f;
           if (!live) d[v] = 0.0f;
         }
         if (p.accumulate) {
@@ -487,7 +513,7 @@ template <class T, int V, bool VEC, bool SIGMOID>
 cudaError_t launch_one(const BalanceParams& p, bool backward, cudaStream_t s) {
   if (backward) {
     // 32 warps an SM, and no more than 8 tokens each
-    const int tokens = std::min(std::max(p.n / (32 * p.num_sms), at_once(V)), 8), per = kBackWarps * tokens;
+    const int tokens = std::min(std::max(p.n / (64 * p.num_sms), 1), 8), per = kBackWarps * tokens;
     return launch_pdl(balance_backward_kernel<T, V, VEC, SIGMOID>, (p.n + per - 1) / per, kBackWarps, 0, s, p, tokens);
   }
   return BalanceAlone(p) ? launch_sums<T, V, VEC, SIGMOID, true>(p, s) : launch_sums<T, V, VEC, SIGMOID, false>(p, s);
