@@ -48,6 +48,9 @@ struct I8ProductParams {
 };
 
 cudaError_t LaunchI8Product(const I8ProductParams& p, cudaStream_t s);
+// Dense products of up to kI8FewTokens tokens, where LaunchI8Product finds that cheaper.
+constexpr int kI8FewTokens = 24;
+cudaError_t LaunchI8Few(const I8ProductParams& p, int device, int sms, cudaStream_t s);
 // Read and clear the current device's error word of the products, in order on s.
 cudaError_t ReadI8Error(int32_t* value, cudaStream_t s);
 

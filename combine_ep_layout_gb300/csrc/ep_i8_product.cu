@@ -36,6 +36,7 @@
 #include <cstdint>
 
 #include "ep_gb300_i8.h"
+#include "ep_i8_act.cuh"
 #include "ep_i8_kernels.hpp"
 #include "ep_i8_mma.cuh"
 #include "ep_kernels.hpp"
@@ -150,18 +151,6 @@ __device__ __forceinline__ uint4 read16(uint32_t addr) {
 }
 __device__ __forceinline__ void write16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// v sigmoid(s): silu with s = v; the tanh form of gelu is the same with
-// s = 2 sqrt(2 / pi) (v + 0.044715 v^3), as (1 + tanh(u)) / 2 is sigmoid(2 u).  The exponential
-// is off by 2^-22 and by the rounding of its argument, |s| 2^-23, which sigmoid's slope takes
-// to under 4 2^-24 of |v|.
-__device__ __forceinline__ float activate(int act, float v) {
-  const float s = act == EP_ACT_SILU ? v : v * fmaf(0.07135481282553f * v, v, 1.5957691216057308f);
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * s));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return v * r;
 }
 
 // A warp's 8 N tokens of 32 channels, as fragments: y[h][i][e] is channel 16 h + lane / 4 + 8 (e / 2) of
@@ -492,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float v = theirs[32 * j + lane], own = gate ? y[j >> 3][j >> 2 & 1][j & 3] : y[j >> 3][2 + (j >> 2 & 1)][j & 3];
-            h[j >> 3][j >> 2 & 1][j & 3] = activate(a.p.act, gate ? own : v) * (gate ? v : own);
+            h[j >> 3][j >> 2 & 1][j & 3] = i8_activate(a.p.act, gate ? own : v) * (gate ? v : own);
           }
           __syncwarp();
           if (lane == 0) tma::mbar_arrive(swap_done(other));
@@ -596,13 +585,13 @@ cudaError_t launch(Args& a, const Gpu& gpu, int64_t most_tiles, cudaStream_t s) 
 // and its share of the memory's rate; the ends are set-up and output, which up to
 // 128 tokens run beside the next tile.
 int64_t tile_cost(int width, int part, int steps) {
-  const int products = 8 * (9 + width / 2), widen = 330 + 3 * width / 2, bytes = 2 * part * kStep / 22;
-  return static_cast<int64_t>(steps) * std::max(products, std::max(widen, bytes)) + (width > 128 ? 6000 : 2000);
+  const int products = 8 * (9 + width / 2), widen = 390 + 3 * width / 2, bytes = 2 * part * kStep / 22;
+  return static_cast<int64_t>(steps) * std::max(products, std::max(widen, bytes)) + (width > 128 ? 6000 : 4000);
 }
 
 // Tokens of a tile and weight rows of a half tile of a dense product: what takes the fewest cycles
 // when each pair of SMs takes its share of the tiles in turn.
-void choose(int64_t n, int channels, bool gated, int steps, int pairs, int* nt, int* part) {
+int64_t choose(int64_t n, int channels, bool gated, int steps, int pairs, int* nt, int* part) {
   int64_t least = INT64_MAX;
   const int per = gated ? 2 : 4;             // channels of a pair tile for each row of a half tile
   for (int t = 32; t <= 256; t *= 2) {
@@ -614,6 +603,7 @@ void choose(int64_t n, int channels, bool gated, int steps, int pairs, int* nt, 
       if (cost < least) least = cost, *nt = t, *part = m;
     }
   }
+  return least;
 }
 
 }  // namespace
@@ -630,7 +620,12 @@ cudaError_t LaunchI8Product(const I8ProductParams& p, cudaStream_t s) {
   int nt = 256;
   a.part = kRows / 2;
   if (!p.first) {
-    choose(p.n, channels, gated, a.steps, gpu.sms / 2, &nt, &a.part);
+    const int64_t cost = choose(p.n, channels, gated, a.steps, gpu.sms / 2, &nt, &a.part);
+    // beginning and end take this kernel some 8000 cycles, the other one half of that; that one reaches
+    // half of the integer rate, for whole column tiles of 8 tokens
+    if (p.n <= kI8FewTokens &&
+        2 * static_cast<int64_t>(p.rows) * p.cols * ((p.n + 7) / 8 * 8) / (261 * gpu.sms) + 4000 < cost + 8000)
+      return LaunchI8Few(p, gpu.device, gpu.sms, s);
   } else {
     // the average expert's rows, and some more, in one tile
     const int64_t mean = p.entries / p.experts + 1;
