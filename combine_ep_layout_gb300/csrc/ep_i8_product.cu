@@ -11,13 +11,13 @@
 // are the operand in tensor memory, where their fp16 form costs shared memory neither a write
 // nor a read; x is the operand in shared memory, each CTA widening half of it.  With the
 // weights along the 256 rows of the instruction, the number of tokens of a tile is free (a multiple of
-// 32), which experts with few tokens need.  Roles of a CTA's 28 warps:
+// 32), which experts with few tokens need.  Roles of a CTA's 32 warps:
 //   0       TMA loads of both operands, a ring of 128 columns a stage
 //   1       (first CTA) issues the products
 //   2       tensor memory
 //   4-19    widen, in groups that take the stages in turn, as a stage's latency (reads, fence,
 //           tensor memory, barriers) is a multiple of its work: 32 weight rows a warp, and a share of x
-//   20-27   sums times scales, activation, output; up to 128 tokens the sums are double
+//   20-31   sums times scales, activation, output; up to 128 tokens the sums are double
 //           buffered, so that this runs beside the next tile
 // A CTA's rows are two half tiles of up to 64, in the lanes from 0 and from 64 on: gated, the
 // second half is the up rows of the first, and the warps that hold them swap halves through
@@ -48,7 +48,7 @@ namespace {
 __device__ int32_t g_error;
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kWideners = 16, kWriters = 8;   // warps
+constexpr int kWideners = 16, kOfQuad = 2, kWriters = 4 * kOfQuad;   // warps; writing ones of 32 lanes of tensor memory
 constexpr int kFirstWriter = 4 + kWideners, kThreads = 32 * (kFirstWriter + kWriters);
 constexpr int kRows = 128;                 // weight rows of a CTA
 constexpr int kStep = 128;                 // columns of a stage
@@ -64,9 +64,13 @@ __host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : nt
 __host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }         // sum buffers
 __host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
 __host__ __device__ constexpr int bytes_out(int nt) { return nt / 2 * kStep * 2; }
+// Rows of x come in boxes of 32, as many as the tile has.  Widening 256 tokens' rows for 192 took as long as 256
+// tokens do: shared memory moves 128 bytes a cycle and a stage needs 112 KB of it (copies, reads, widened writes,
+// and what the products read), 1000 cycles where the products of 192 tokens take 840.
+__host__ __device__ constexpr int x_box(int nt) { return nt / 2 < 32 ? nt / 2 : 32; }
 constexpr int kSwap = 16 * 32 * 4;         // what a writing warp hands over, or 32 tokens of its output
-constexpr int kBarBytes = 528;
-constexpr int kScaleBytes = 4 * 32 * 4;    // a writing warp's scales of x
+constexpr int kBarBytes = 592;             // and 16 words: a stage's rows of x
+constexpr int kScaleBytes = (8 + kOfQuad - 1) / kOfQuad * 32 * 4;    // a writing warp's scales of x
 constexpr int kFixed = kWriters * kSwap + kWriters * kScaleBytes + kBarBytes;
 
 struct Args {
@@ -209,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   constexpr int kGroups = groups(NT), kOfStage = kWideners / kGroups;      // warps of a stage
   static_assert(kS2 >= kGroups && kD * NT + kS2 * kColumnsA <= static_cast<int>(kTmem));
   constexpr uint32_t kSumColumns = kD * NT;
+  constexpr int kBox = x_box(NT);
   extern __shared__ uint8_t raw[];
   __shared__ int dead;
   __shared__ uint32_t tmem_at;
@@ -228,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   const auto swap_ready = [&](int s) { return bars + 384 + 8 * s; };
   const auto swap_done = [&](int s) { return bars + 448 + 8 * s; };
   const uint32_t end_bar = bars + 512;
+  const auto x_rows = [&](int s) { return bars + 528 + 4 * s; };   // rows of x in a stage of the int8 ring
 
   if (threadIdx.x == 0) {
     dead = 0;
@@ -280,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   if (warp == 0) {
     // as for the products, the whole warp goes along and one elected lane issues
     const bool one = pair::elect();
-    const uint32_t bytes = 2 * a.part * kStep + kTok * kStep;
     int in = 0;
     uint32_t turn = 0, copies = 0;
     bool ok = true;
@@ -288,15 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       const Tile t = tile_of(tile);
       const int lead = (2 * t.row_tile + static_cast<int>(cta)) * (GATED ? a.part : 2 * a.part);
       const int y0 = t.expert * a.p.rows + lead, y1 = y0 + (GATED ? half : a.part);
-      const int yx = t.first + static_cast<int>(cta) * (t.width / 2);
+      const int yx = t.first + static_cast<int>(cta) * (t.width / 2), boxes = (t.width / 2 + kBox - 1) / kBox;
+      const uint32_t bytes = (2 * a.part + boxes * kBox) * kStep;
       for (int k = 0; k < a.steps; ++k) {
         if (!(ok = __all_sync(kAll, wait(empty_in(in), turn ^ 1)))) break;
         if (one) {
           const uint32_t at = base + in * kIn, bar = full_in(in);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(x_rows(in)), "r"(boxes * kBox) : "memory");
           tma::mbar_expect_tx(bar, bytes);
           pair::load_box(at, &a.w, k * kStep, y0, bar);
           pair::load_box(at + kRows / 2 * kStep, &a.w, k * kStep, y1, bar);
-          pair::load_box(at + kRows * kStep, &a.x, k * kStep, yx, bar);
+#pragma unroll
+          for (int i = 0; i < kTok / kBox; ++i)
+            if (i < boxes) pair::load_box(at + (kRows + i * kBox) * kStep, &a.x, k * kStep, yx + i * kBox, bar);
         }
         __syncwarp();
         copies = min(copies + 1, static_cast<uint32_t>(s1));
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
     constexpr int kMineA = 32 / kOfStage;      // 16-column chunks of a row of w that a thread widens
     constexpr int kRowParts = 32 * kOfStage / kTok, kMine = kRowParts < 8 ? 8 / kRowParts : 1;   // threads of a row of x, its chunks of a thread
     const int thread = 32 * w + lane, xrow = thread % kTok, xpart = thread / kTok;
-    const bool has_x = xpart < 8, has_rows = a.part > 32 * (quad & 1);
+    const bool has_rows = a.part > 32 * (quad & 1);
     const uint32_t to = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kSumColumns + part * 8 * kMineA;
     const uint32_t from_a = base + row * kStep, from_x = base + kRows * kStep + xrow * kStep;
     const uint32_t to_x = out0 + xrow * 128;
@@ -360,12 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
     const int64_t all = first_tile < total ? static_cast<int64_t>((total - first_tile + pairs - 1) / pairs) * a.steps : 0;
     bool ok = true;
     for (int64_t it = group; it < all; it += kGroups) {
-      // In this order: where the int8 ring has an odd number of stages the groups take turns on
-      // each of them, and the parity alone cannot tell the copy meant from one before the last.  The
-      // products of kS2 stages ago are done here, so the copy before is behind (s1 >= kS2).
-      ok = __all_sync(kAll, wait(empty_out(out), out_turn ^ 1) && wait(full_in(in), in_turn));
+      // Where the int8 ring has a number of stages that the groups do not divide, they take turns on
+      // each of them, and a parity alone cannot tell the copy meant from the one before: so the one before
+      // has to have been read.
+      ok = __all_sync(kAll, wait(empty_in(in), in_turn ^ 1) && wait(full_in(in), in_turn));
       if (!ok) break;
-      pair::fence_after();
+      uint32_t there;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(there) : "r"(x_rows(in)) : "memory");
+      const bool has_x = xpart < 8 && xrow < static_cast<int>(there);
       uint4 va[kMineA], vx[kMine];
       if (has_rows)
 #pragma unroll
@@ -373,6 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
         if (has_x) vx[i] = read16(from_x + in * kIn + (((xpart + i * kRowParts) ^ (xrow & 7)) << 4));
+      __syncwarp();
+      if (lane == 0) tma::mbar_arrive(empty_in(in));
+      ok = __all_sync(kAll, wait(empty_out(out), out_turn ^ 1));
+      if (!ok) break;
+      pair::fence_after();
       if (has_rows)
 #pragma unroll
       for (int c = 0; c < kMineA; c += 2) {
@@ -403,10 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       pair::wait_st();
       pair::fence_before();
       __syncwarp();
-      if (lane == 0) {
-        tma::mbar_arrive(empty_in(in));
-        pair::arrive_remote(pair::in_cta(full_out(out), 0));
-      }
+      if (lane == 0) pair::arrive_remote(pair::in_cta(full_out(out), 0));
       if ((in += kGroups) >= s1) in -= s1, in_turn ^= 1;
       if ((out += kGroups) >= kS2) out -= kS2, out_turn ^= 1;
     }
@@ -415,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       for (int64_t j = all > kS2 ? all - kS2 : 0; j < all; ++j)
         tma::mbar_wait_bounded(empty_out(static_cast<int>(j % kS2)), static_cast<uint32_t>(j / kS2) & 1, tma::kDrainNs);
   } else if (warp >= kFirstWriter) {
-    const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;
+    const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;   // other: of the same tokens
     const int out_rows = GATED ? half : a.p.rows;
     const bool gate = quad < 2;                // (not gated: the first half tile)
     // this warp's scales of x, and what it hands over and is handed
@@ -440,20 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
         ws[g] = at < channels ? ld_coherent(a.p.w_scales + static_cast<int64_t>(t.expert) * a.p.rows + row + at) : 0.0f;
       }
       __syncwarp();
-      for (int i = 0, c = 32 * which + lane; c < t.width; ++i, c += 64)
+      for (int i = 0, c = 32 * which + lane; c < t.width; ++i, c += 32 * kOfQuad)
         xs[32 * i + lane] = c < t.tokens ? ld_coherent(a.p.x_scales + t.first + c) : 0.0f;
       __syncwarp();
       ok = __all_sync(kAll, wait(full_sum(buf), buf_turn));
       if (!ok) break;
       pair::fence_after();
       if (32 * which >= t.width && lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));   // nothing here for it
-      for (int i = 0, c = 32 * which; c < t.width; ++i, c += 64) {
+      for (int i = 0, c = 32 * which; c < t.width; ++i, c += 32 * kOfQuad) {
         uint32_t r[2][16];
         const uint32_t from = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * NT + c;
         pair::ld16x32(from, r[0]);
         pair::ld16x32(from + (16u << 16), r[1]);
         pair::wait_ld();
-        if (c + 64 >= t.width) {               // the sums may be overwritten
+        if (c + 32 * kOfQuad >= t.width) {               // the sums may be overwritten
           pair::fence_before();
           __syncwarp();
           if (lane == 0) pair::arrive_remote(pair::in_cta(empty_sum(buf), 0));
@@ -554,9 +567,9 @@ cudaError_t launch(Args& a, const Gpu& gpu, int64_t most_tiles, cudaStream_t s) 
   const int starts = a.p.first ? 4 * (a.p.experts + 1) : 0;
   const int room = kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - starts;
   a.stages_in = std::min(16, room / bytes_in(NT));
-  static_assert((kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - 4 * 2049) / bytes_in(NT) >= stages_out(NT));
+  static_assert((kMaxShared - kFixed - stages_out(NT) * bytes_out(NT) - 4 * 2049) / bytes_in(NT) >= 2);
   const int smem = 1024 + a.stages_in * bytes_in(NT) + stages_out(NT) * bytes_out(NT) + kFixed + starts;
-  if (const cudaError_t e = map_of(&a.x, a.p.x, a.p.n, a.p.cols, NT / 2); e != cudaSuccess) return e;
+  if (const cudaError_t e = map_of(&a.x, a.p.x, a.p.n, a.p.cols, x_box(NT)); e != cudaSuccess) return e;
   if (const cudaError_t e = map_of(&a.w, a.p.w, static_cast<int64_t>(a.p.experts) * a.p.rows, a.p.cols, a.part); e != cudaSuccess) return e;
   // the kernel's shared-memory limit is raised once on each device
   static std::atomic<uint64_t> ready{0};
