@@ -141,10 +141,5 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-// The same, in this CTA only.
-__device__ __forceinline__ void commit_here(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 }  // namespace pair
 }  // namespace epg

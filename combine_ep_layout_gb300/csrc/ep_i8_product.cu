@@ -57,9 +57,9 @@ constexpr uint32_t kTmem = 512;
 constexpr int kMaxShared = 232448 - 1024 - 64;   // less what aligning the buffers may take, and static data
 
 // Groups of widening warps that take the stages in turn, and widened stages: as many as tensor memory
-// holds beside the sums, up to 6.  Up to 64 tokens a stage's latency is what counts (4 groups; with 2
-// 16 tokens x 2048 x 7168 took 27 us).
-__host__ __device__ constexpr int groups(int nt) { return nt <= 64 ? 4 : 2; }
+// holds beside the sums, and shared memory, up to 6.  Up to 128 tokens a stage's latency counts for more than
+// its work: 4 groups (gated 333 x 11008 x 4096: 32 us, with 2 groups 35; 45 x 20011 x 4096: 28.6 and 31.6).
+__host__ __device__ constexpr int groups(int nt) { return nt <= 128 ? 4 : 2; }
 __host__ __device__ constexpr int stages_out(int nt) { return nt == 256 ? 3 : nt == 128 ? 4 : 6; }
 __host__ __device__ constexpr int sums(int nt) { return nt == 256 ? 1 : 2; }         // sum buffers
 __host__ __device__ constexpr int bytes_in(int nt) { return kRows * kStep + nt / 2 * kStep; }
@@ -125,12 +125,13 @@ struct Waits {
   uint64_t limit;
 
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (pair::try_wait(bar, parity)) return true;
-    const uint64_t t0 = tma::global_ns();
-    for (;;) {
-      if (*dead) return false;
-      if (limit != 0 && pair::try_wait(bar, parity)) return true;
-      if (limit == 0 || tma::global_ns() - t0 > limit) break;
+    if (limit == 0 ? tma::mbar_test(bar, parity) : pair::try_wait(bar, parity)) return true;
+    if (limit != 0) {
+      const uint64_t t0 = tma::global_ns();
+      do {
+        if (*dead) return false;
+        if (pair::try_wait(bar, parity)) return true;
+      } while (tma::global_ns() - t0 <= limit);
     }
     *dead = 1;
     atomicOr(&g_error, kErrTimeout);
@@ -349,10 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
         __syncwarp();
         if (++buf == kD) buf = 0, buf_turn ^= 1;
       }
-      // the products in flight end before the tensor memory is freed
-      if (one) pair::commit_here(end_bar);
+      if (one) pair::commit(end_bar);
       __syncwarp();
-      tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
     }
   } else if (warp >= 4 && warp < kFirstWriter) {
     const int w = (warp - 4) % kOfStage, group = (warp - 4) / kOfStage, quad = w & 3, part = w >> 2, row = 32 * quad + lane;
@@ -423,10 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
       if ((in += kGroups) >= s1) in -= s1, in_turn ^= 1;
       if ((out += kGroups) >= kS2) out -= kS2, out_turn ^= 1;
     }
-    // the last arrivals of the other CTA's products reach this one before it ends
-    if (ok && w == 0 && lane == 0)
-      for (int64_t j = all > kS2 ? all - kS2 : 0; j < all; ++j)
-        tma::mbar_wait_bounded(empty_out(static_cast<int>(j % kS2)), static_cast<uint32_t>(j / kS2) & 1, tma::kDrainNs);
   } else if (warp >= kFirstWriter) {
     const int w = warp - kFirstWriter, quad = w & 3, which = w >> 2, other = w ^ 2;   // other: of the same tokens
     const int out_rows = GATED ? half : a.p.rows;
@@ -514,6 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) i8_mma_
   __syncwarp();
   pair::fence_before();
   __syncthreads();
+  // in both CTAs: the products in flight, and their arrivals here, are over before this block's memory goes
+  if (warp == 1) tma::mbar_wait_bounded(end_bar, 0, tma::kDrainNs);
+  __syncwarp();
   pair::cluster_sync();
   pair::fence_after();
   if (warp == 2) pair::dealloc(tmem, kTmem);
@@ -633,12 +631,13 @@ cudaError_t LaunchI8Product(const I8ProductParams& p, cudaStream_t s) {
   int nt = 256;
   a.part = kRows / 2;
   if (!p.first) {
-    const int64_t cost = choose(p.n, channels, gated, a.steps, gpu.sms / 2, &nt, &a.part);
     // beginning and end take this kernel some 8000 cycles, the other one half of that; that one reaches
     // half of the integer rate, for whole column tiles of 8 tokens
-    if (p.n <= kI8FewTokens &&
-        2 * static_cast<int64_t>(p.rows) * p.cols * ((p.n + 7) / 8 * 8) / (261 * gpu.sms) + 4000 < cost + 8000)
-      return LaunchI8Few(p, gpu.device, gpu.sms, s);
+    const int64_t few = 2 * static_cast<int64_t>(p.rows) * p.cols * ((p.n + 7) / 8 * 8) / (261 * gpu.sms) + 4000;
+    const bool can = p.n <= kI8FewTokens;
+    if (can && few < tile_cost(32, 8, a.steps) + 8000) return LaunchI8Few(p, gpu.device, gpu.sms, s);   // no tile takes less
+    const int64_t cost = choose(p.n, channels, gated, a.steps, gpu.sms / 2, &nt, &a.part);
+    if (can && few < cost + 8000) return LaunchI8Few(p, gpu.device, gpu.sms, s);
   } else {
     // the average expert's rows, and some more, in one tile
     const int64_t mean = p.entries / p.experts + 1;
