@@ -7,7 +7,8 @@
  * The conventions are those of ep_gb300.h: device pointers of the current
  * device, work enqueued on `stream`, no synchronisation and no allocation in
  * the calls that do work (they can be captured into a CUDA graph), 0 or a
- * negative EP_E* code returned with a message from ep_last_error().
+ * negative EP_E* code returned with a message from ep_last_error().  No output
+ * may overlap an input.
  */
 #ifndef EP_GB300_I8_H
 #define EP_GB300_I8_H

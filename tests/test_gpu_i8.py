@@ -191,7 +191,8 @@ def check_linear(n, rows, cols, act=None, dtype=torch.bfloat16, most=127, make=w
     (1, 1, 16), (1, 64, 64), (2, 17, 48), (3, 129, 80), (1, 4096, 1024), (5, 257, 2064), (8, 1000, 512), (9, 255, 144),
     (16, 640, 4096), (17, 300, 1040), (31, 70, 256), (33, 513, 336), (63, 2048, 1024), (64, 128, 7168), (65, 260, 400),
     (100, 1024, 640), (127, 511, 1264), (129, 256, 128), (200, 2000, 912), (255, 130, 256), (256, 256, 2048),
-    (257, 1281, 336), (500, 384, 1600), (1023, 520, 208), (0, 64, 64)])
+    (257, 1281, 336), (500, 384, 1600), (1023, 520, 208), (0, 64, 64), (100, 1, 16), (24, 4099, 112), (25, 90, 16),
+    (40, 30001, 64), (3001, 17, 4096)])
 def test_linear(n, rows, cols, dtype):
     check_linear(n, rows, cols, None, dtype)
 
