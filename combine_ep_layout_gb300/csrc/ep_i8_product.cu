@@ -11,13 +11,13 @@
 // are the operand in tensor memory, where their fp16 form costs shared memory neither a write
 // nor a read; x is the operand in shared memory, each CTA widening half of it.  With the
 // weights along the 256 rows of the instruction, the number of tokens of a tile is free (a multiple of
-// 32), which experts with few tokens need.  Roles of a CTA's 32 warps:
+// 32), which experts with few tokens need.  Roles of a CTA's 28 warps:
 //   0       TMA loads of both operands, a ring of 128 columns a stage
 //   1       (first CTA) issues the products
 //   2       tensor memory
 //   4-19    widen, in groups that take the stages in turn, as a stage's latency (reads, fence,
 //           tensor memory, barriers) is a multiple of its work: 32 weight rows a warp, and a share of x
-//   20-31   sums times scales, activation, output; up to 128 tokens the sums are double
+//   20-27   sums times scales, activation, output; up to 128 tokens the sums are double
 //           buffered, so that this runs beside the next tile
 // A CTA's rows are two half tiles of up to 64, in the lanes from 0 and from 64 on: gated, the
 // second half is the up rows of the first, and the warps that hold them swap halves through
