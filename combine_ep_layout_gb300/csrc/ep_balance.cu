@@ -12,7 +12,7 @@
 // pairs (block, sequence) with tokens form a staircase, so block + sequence numbers their
 // rows.  Every sum has a fixed order; only whole numbers go through atomics.
 //
-// Backward: a warp takes up to 8 consecutive tokens, a few at a time, with the counts of their
+// Backward: a warp takes up to 16 consecutive tokens, a few at a time, with the counts of their
 // sequence in registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -450,16 +450,17 @@ __global__ void __launch_bounds__(kBackWarps * 32, V <= 8 ? 6 : 1) balance_backw
         const bool live = __any_sync(kAll, id[u] >= 0);
         if (!live && p.accumulate) continue;
         T* out = static_cast<T*>(p.grad) + (t + u) * p.grad_stride;
-        const float lse = peak[u] + __shfl_sync(kAll, my_log, U == 1 ? 0 : u), rise = whole[u] > 0.0f ? gz * lse : 0.0f;
+        // finite, as an infinite one would make the other scores' 0 a NaN
+        const float lse = fminf(peak[u] + __shfl_sync(kAll, my_log, U == 1 ? 0 : u), 3e38f);
+        const float rise = live && whole[u] > 0.0f ? gz * lse : 0.0f, part = live ? share : 0.0f;
         float d[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float q = z[u][v];
+          const float apart = c[v] - dot[u];
           if constexpr (SIGMOID)
-            d[v] = share * q * (c[v] - dot[u]) * not_s[u][v] + (soft[u][v] > 0.0f ? rise * soft[u][v] : 0.0f);
+            d[v] = fmaf(part * apart, z[u][v] * not_s[u][v], rise * soft[u][v]);
           else
-            d[v] = q > 0.0f ? q * fmaf(share, c[v] - dot[u], rise) : 0.0f;
-          if (!live) d[v] = 0.0f;
+            d[v] = z[u][v] * fmaf(part, apart, rise);
         }
         if (p.accumulate) {
 #pragma unroll
@@ -512,8 +513,8 @@ cudaError_t launch_sums(const BalanceParams& p, cudaStream_t s) {
 template <class T, int V, bool VEC, bool SIGMOID>
 cudaError_t launch_one(const BalanceParams& p, bool backward, cudaStream_t s) {
   if (backward) {
-    // 32 warps an SM, and no more than 8 tokens each
-    const int tokens = std::min(std::max(p.n / (64 * p.num_sms), 1), 8), per = kBackWarps * tokens;
+    // 32 warps an SM, and no more than 16 tokens each
+    const int tokens = std::min(std::max(p.n / (32 * p.num_sms), 1), 16), per = kBackWarps * tokens;
     return launch_pdl(balance_backward_kernel<T, V, VEC, SIGMOID>, (p.n + per - 1) / per, kBackWarps, 0, s, p, tokens);
   }
   return BalanceAlone(p) ? launch_sums<T, V, VEC, SIGMOID, true>(p, s) : launch_sums<T, V, VEC, SIGMOID, false>(p, s);
