@@ -170,15 +170,6 @@ __device__ __forceinline__ int sequence_of(const BalanceParams& p, int t, int la
   return lo;
 }
 
-// Brings a run of rows to L2 ahead of everything that the first loads wait for (a hint).
-template <class T>
-__device__ __forceinline__ void prefetch_rows(const BalanceParams& p, int start, int end) {
-  if (start >= end || p.row_stride > 2 * p.experts) return;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + start * p.row_stride) & ~static_cast<uintptr_t>(15);
-  const uintptr_t b = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.logits) + (end - 1) * p.row_stride + p.experts);
-  prefetch_l2(reinterpret_cast<const void*>(a), static_cast<uint32_t>((b - a) & ~static_cast<uintptr_t>(15)));
-}
-
 // A lane's choice of a token, -1 where it is no expert.
 __device__ __forceinline__ int id_of(const BalanceParams& p, const int64_t* at) {
   const uint64_t id = static_cast<uint64_t>(*at);
@@ -266,7 +257,6 @@ __global__ void __launch_bounds__(sum_warps(V) * 32) balance_sums_kernel(Balance
   int* cnt = reinterpret_cast<int*>(shared + kWarps * p.experts);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int run = run_of(p.n, p.blocks), start = static_cast<int>(blockIdx.x) * run, end = min(start + run, p.n);
-  if (threadIdx.x == 0) prefetch_rows<T>(p, start, end);
   grid_dependency_wait();
   __shared__ int found[3];
   for (int at = start; at < end;) {
