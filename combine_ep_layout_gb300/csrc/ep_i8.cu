@@ -76,14 +76,14 @@ __device__ __forceinline__ uint4 round16(const float (&v)[kVec], float s, float 
 }
 
 // How the columns lie among a row's threads.  kTogether: 16 consecutive ones a thread, whose int8 are one store;
-// kSpread (fp32 in place): four times 4, G threads side by side, so that a load's 32 lanes read 512 bytes in a
-// row (1001 x 14336: 15.6 us, together 21.4).  kSingle: as kTogether, value by value (not 16-byte aligned).
+// kSpread (in place): four times 4 fp32 or twice 8 bf16, G threads side by side, so that a load's 32 lanes read
+// 512 bytes in a row (1001 x 14336: 15.6 us, together 21.4).  kSingle: as kTogether, value by value (not 16-byte aligned).
 enum Lie { kTogether, kSpread, kSingle };
 
 // G threads a row, 128 / G rows a block where G is below 128.
 template <class T, int G, int MINE, Lie LIE>
 __global__ void __launch_bounds__(G < 128 ? 128 : G, (MINE == 1 ? 1536 : 1024) / (G < 128 ? 128 : G)) i8_rows_kernel(I8RowsParams p) {
-  constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G;
+  constexpr int kThreads = G < 128 ? 128 : G, kRows = kThreads / G, kPer = 16 / sizeof(T);
   constexpr bool kMore = MINE == 2;           // rows may have more vectors than the threads hold
   __shared__ unsigned most[2][kThreads / 32];
   allow_dependent_grids();
@@ -104,11 +104,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, (MINE == 1 ? 1536 : 1024) /
     auto load = [&](int c, float(&a)[kVec]) {
       if constexpr (LIE == kSpread) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 16 * G * c + 4 * G * i + 4 * at;
-          float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (ok && col < p.cols) f = *reinterpret_cast<const float4*>(x + col);
-          a[4 * i] = f.x, a[4 * i + 1] = f.y, a[4 * i + 2] = f.z, a[4 * i + 3] = f.w;
+        for (int i = 0; i < kVec / kPer; ++i) {
+          const int col = 16 * G * c + kPer * G * i + kPer * at;
+          uint4 f = make_uint4(0, 0, 0, 0);
+          if (ok && col < p.cols) f = *reinterpret_cast<const uint4*>(x + col);
+          const T* e = reinterpret_cast<const T*>(&f);
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) a[kPer * i + j] = rows::as_float(e[j]);
         }
       } else if (ok && c * G + at < vectors) {
         load16<T, LIE == kTogether>(x + static_cast<int64_t>(c * G + at) * kVec, a);
@@ -147,9 +149,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, (MINE == 1 ? 1536 : 1024) /
       if constexpr (LIE == kSpread) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 16 * G * c + 4 * G * i + 4 * at;
-          if (col < p.cols) *reinterpret_cast<uint32_t*>(p.q + row * p.cols + col) = w[i];
+        for (int i = 0; i < kVec / kPer; ++i) {
+          const int col = 16 * G * c + kPer * G * i + kPer * at;
+          if (col >= p.cols) continue;
+          if constexpr (kPer == 4)
+            *reinterpret_cast<uint32_t*>(p.q + row * p.cols + col) = w[i];
+          else
+            *reinterpret_cast<uint2*>(p.q + row * p.cols + col) = make_uint2(w[2 * i], w[2 * i + 1]);
         }
       } else if (!p.slots) {
         if (vector < vectors) *reinterpret_cast<uint4*>(to + row * p.cols) = q;
@@ -192,8 +198,7 @@ cudaError_t launch_g(const I8RowsParams& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   if (!vec) return cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, kSingle>, p);
-  if (sizeof(T) == 4 && !p.slots)
-    if constexpr (sizeof(T) == 4) return cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, kSpread>, p);
+  if (!p.slots) return cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, kSpread>, p);
   return cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, G, MINE, kTogether>, p);
 }
 
