@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kFinalWarps * 32) balance_final_kernel(Balance
 }
 
 template <class T, int V, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kBackWarps * 32, V <= 8 ? 6 : 1) balance_backward_kernel(BalanceParams p, int tokens) {
+__global__ void __launch_bounds__(kBackWarps * 32, V > 8 ? 1 : SIGMOID ? 4 : 6) balance_backward_kernel(BalanceParams p, int tokens) {
   constexpr int U = V <= 4 ? 2 : 1;          // more registers cost more than they bring (256 experts, two rows: 24 us, one: 20)
   allow_dependent_grids();
   const int lane = threadIdx.x & 31;
