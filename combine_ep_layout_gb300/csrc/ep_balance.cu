@@ -14,6 +14,11 @@
 //
 // Backward: a warp takes up to 16 consecutive tokens, a few at a time, with the counts of their
 // sequence in registers.
+//
+// Measured: 32768 x 256 fp32 scores, 8 sequences, both directions 39.5 us (1.75 TB/s); cold 17 us the sums
+// (171 instructions a token, 41% of the issue slots while active), 7 the second launch, 17 the gradient
+// (266 instructions a token, 49%).  What bounds them is latency: a block's search, rows, sums and output follow
+// each other.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

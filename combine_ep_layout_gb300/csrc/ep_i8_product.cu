@@ -23,6 +23,13 @@
 // second half is the up rows of the first, and the warps that hold them swap halves through
 // shared memory.  Where rows are few, half tiles are smaller, so that every SM has some.
 //
+// Measured: 8192 x 7168 x 7168 451 us (1.87 PFLOP/s, 97% of the library's bf16 rate; the tensor cores 87% of
+// their cycles at 2048 tokens), where the products of a stage, 8 x 137 cycles, are what bounds it; 64 tokens over 64
+// experts of 7168 x 4096, gated, top-8, 270 us (7.0 TB/s of weights); 8192 tokens over 128 experts of 4096 x 2816,
+// gated, top-6, 823 us (1.38 PFLOP/s: tiles of 192 tokens, whose stages shared memory bounds, and their ends); 45 x
+// 20011 x 4096 27.4 us (a stage's latency, 650 cycles for 330 of products).  A fetch of the next tile's
+// rows hides behind the rings; the ends of a tile do not where its sums are not double buffered.
+//
 // Every wait is bounded.  A warp that gives up records it, marks its CTA and leaves; the
 // others of the pair give up by the mark or by their own limit, and all meet before the
 // tensor memory is freed.
