@@ -286,6 +286,26 @@ def test_grouped_routings(shares):
         check_grouped(h, 320, 400, act, torch.bfloat16)
 
 
+def test_grouped_behind_two_gigabytes():
+    """Experts whose weights begin past 32 bits of bytes."""
+    E, rows, cols = 40, 4096, 16384
+    w = torch.zeros((E, rows, cols), dtype=torch.int8, device="cuda")
+    for e in (0, 31, 32, 39):
+        w[e] = whole((rows, cols), e, 9)
+    ws = scales((E, rows), 1)
+    h, _ = handle(90, E, 2, 8, masked=0.0)
+    x, xs = whole((h.recv_capacity, cols), 2, 9), scales((h.recv_capacity,), 3)
+    out = torch.zeros((h.recv_capacity, rows), dtype=torch.bfloat16, device="cuda")
+    ep.ep_i8_grouped(h, x, xs, w, ws, out)
+    first, count = h.field(ep.FIELD_PSUM_PER_EXPERT).tolist(), h.field(ep.FIELD_NUM_UNALIGNED_PER_EXPERT).tolist()
+    for e in range(E):
+        a, b = first[e], first[e] + count[e]
+        if e in (0, 31, 32, 39):
+            agree(out[a:b], x[a:b], xs[a:b], w[e], ws[e], None)
+        else:
+            assert (out[a:b] == 0).all()
+
+
 def test_products_in_a_graph_on_two_streams():
     """Captured products replayed beside eager ones on another stream: equal bits."""
     calls = []
